@@ -147,6 +147,53 @@ asr_status asr_op_attention(const void* qkv, const int32_t* cu, int n_seg, int m
  * output for |x| >= 0.5.  x, y: device float32 [n]. */
 asr_status asr_op_gelu(const float* x, float* y, int64_t n, void* stream);
 
+/* ---- fp8 dense layer ---------------------------------------------------------
+ * Quantise a matrix to e4m3 codes with one power-of-two scale per block of
+ * block_rows rows x 128 columns:
+ *   s     = the smallest integer in [-127, 120] with max |x| <= 448 * 2^s over
+ *           the block's finite values (448 is e4m3's largest; 0 for a block
+ *           of zeros)
+ *   code  = x * 2^-s rounded to e4m3, to nearest, ties to even (the product
+ *           is exact); NaN where x is NaN or infinite
+ *  x          device [M, K] of x_dtype (ASR_DTYPE_BF16, _F16 or _F32), row
+ *             stride ldx elements.
+ *  block_rows 1 (activations) or 128 (weights).
+ *  codes      device e4m3 bytes [M, K], contiguous rows.
+ *  scales     device E8M0 bytes [ceil(M / block_rows), ceil(K / 128)],
+ *             byte = s + 127.
+ * Limits: M, K >= 1, K % 16 == 0, ldx >= K with rows of whole 16 bytes, x and
+ * codes 16-byte aligned (ASR_E_INVAL otherwise); at most 2^31 - 1 blocks of
+ * 1 x 128 (ASR_E_UNSUPPORTED).  Allocates nothing, asynchronous. */
+asr_status asr_op_quantize_fp8(const void* x, int x_dtype, int64_t ldx, int64_t M, int K, int block_rows, void* codes,
+                               void* scales, void* stream);
+
+/* Dense layer on quantised operands: acc = X W^T with the values that codes
+ * and scales stand for, multiplied and scaled on the tensor cores
+ * (tcgen05 kind::mxf8f6f4, fp32 accumulation), then an epilogue of
+ * asr_op_linear.
+ *  x, xs   e4m3 codes [M, K] and E8M0 scales [M, ceil(K / 128)], as
+ *          asr_op_quantize_fp8 writes them with block_rows 1.
+ *  w, ws   e4m3 codes [N, K] and E8M0 scales [ceil(N / 128), ceil(K / 128)]
+ *          (block_rows 128).
+ *  bias    device float32 [N] or NULL.
+ *  epi     ASR_EPI_BF16, ASR_EPI_BF16_GELU, ASR_EPI_F32_RESID, ASR_EPI_F32 or
+ *          ASR_EPI_SWIGLU as for asr_op_linear, or ASR_EPI_F16: y f16 [M, N] =
+ *          acc + bias.
+ *  y       contiguous rows, 16-byte aligned.
+ *  scratch device scratch of >= asr_op_linear_fp8_ws_size() bytes whose first
+ *          int32 is the status word.  Zero it once before its first use: a
+ *          call writes the word only when a bounded device wait gives up, and
+ *          never clears it, so calls on one stream or several may share it
+ *          and one look at the end covers them all.
+ * Limits: M >= 1, K % 16 == 0, N % 16 == 0 (SwiGLU: N % 32 == 0), operands
+ * 16-byte aligned.  A NaN code or scale makes the outputs of its row or
+ * column NaN. */
+enum { ASR_EPI_F16 = 5 };
+size_t asr_op_linear_fp8_ws_size(void);
+asr_status asr_op_linear_fp8(const void* x, const void* xs, const void* w, const void* ws, const float* bias,
+                             int64_t M, int N, int K, int epi, void* y, void* scratch, size_t scratch_bytes,
+                             void* stream);
+
 /* Bounded-wait self-check: launches one kernel that waits on a shared-memory
  * barrier that nothing ever completes, gives up after limit_ns nanoseconds
  * of device time, writes 1 to *status_dev (device int32) and returns

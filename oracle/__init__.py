@@ -20,3 +20,4 @@ Parity status of every function is listed in ``oracle.forward``'s module
 docstring.
 """
 from .forward import *  # noqa: F401,F403
+from .decoder_reads import *  # noqa: F401,F403

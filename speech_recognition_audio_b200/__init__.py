@@ -14,6 +14,7 @@ The entry points mirror ``include/asr_enc.h`` and ``include/asr_ops.h``:
   Encoder.sync_status, set_taps, tap       status word and per-stage taps
   log_mel, linear, layer_norm, attention,
   wait_probe                               kernel-level ops
+  quantize_fp8, linear_fp8                 fp8 operands with a scale per block of 128
   splice_embeddings                        asr_splice_embeddings / asr_splice_check
   Stream(encoder).push / finish            asr_stream_* (live input, window by window)
 """
@@ -23,14 +24,15 @@ import ctypes
 import os
 
 __all__ = ["lib", "LIB_PATH", "AsrError", "Geometry", "tokens", "windows", "weight_names", "Encoder", "Stream",
-           "log_mel", "linear", "linear_tf32", "layer_norm", "attention", "gelu", "wait_probe", "splice_embeddings", "TAP_MEL", "TAP_STEM",
+           "log_mel", "linear", "linear_tf32", "layer_norm", "attention", "gelu", "wait_probe", "splice_embeddings",
+           "quantize_fp8", "linear_fp8", "TAP_MEL", "TAP_STEM",
            "TAP_LAYER0", "TAP_ENCODER", "TAP_HEAD", "EPI_BF16", "EPI_BF16_GELU", "EPI_F32_RESID",
-           "EPI_F32", "EPI_SWIGLU"]
+           "EPI_F32", "EPI_SWIGLU", "EPI_F16"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libasr_enc.so")
 
 TAP_MEL, TAP_STEM, TAP_LAYER0, TAP_ENCODER, TAP_HEAD = range(5)
-EPI_BF16, EPI_BF16_GELU, EPI_F32_RESID, EPI_F32, EPI_SWIGLU = range(5)
+EPI_BF16, EPI_BF16_GELU, EPI_F32_RESID, EPI_F32, EPI_SWIGLU, EPI_F16 = range(6)
 STATUS = {0: "ASR_OK", 1: "ASR_E_INVAL", 2: "ASR_E_UNSUPPORTED", 3: "ASR_E_NOMEM", 4: "ASR_E_CUDA",
           5: "ASR_E_WORKSPACE", 6: "ASR_E_DEVICE_TIMEOUT"}
 
@@ -101,6 +103,9 @@ def _load():
         "asr_op_attention_ws_size": (SZ, []),
         "asr_op_attention": (I, [P, P, I, I, I64, I, P, P, SZ, P]),
         "asr_op_gelu": (I, [P, P, I64, P]),
+        "asr_op_quantize_fp8": (I, [P, I, I64, I64, I, I, P, P, P]),
+        "asr_op_linear_fp8_ws_size": (SZ, []),
+        "asr_op_linear_fp8": (I, [P, P, P, P, P, I64, I, I, I, P, P, SZ, P]),
         "asr_op_wait_probe": (I, [I64, P, P]),
         "asr_stream_window_tokens": (I64, [P]),
         "asr_stream_workspace_size": (SZ, [P, I]),
@@ -457,6 +462,85 @@ def gelu(x, stream=None):
     y = torch.empty_like(x)
     _check(lib.asr_op_gelu(_ptr(x), _ptr(y), x.numel(), _stream(stream)))
     return y
+
+
+def _operands(what, *tensors):
+    """Refuse operands that are not on the current device."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"{what}: every tensor must be on the current CUDA device")
+
+
+def _rows(what, t, cols=None):
+    """Refuse anything but a 2-D tensor of contiguous elements within each row."""
+    if t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1 or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{what}: need a 2-D tensor with contiguous rows" + (f" of {cols}" if cols is not None else ""))
+
+
+def _allocating(stream):
+    """Context in which torch allocates for `stream`, so that what a call allocates and drops is not
+    handed out again before that stream is done with it."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def quantize_fp8(x, block_rows: int = 1, stream=None):
+    """x CUDA [M, K] (bf16 / f16 / f32, rows may be strided) -> (codes float8_e4m3fn [M, K], scales
+    float8_e8m0fnu [ceil(M / block_rows), ceil(K / 128)]), one power-of-two scale per block of block_rows
+    (1 or 128) x 128 (asr_op_quantize_fp8)."""
+    import torch
+    _operands("quantize_fp8", x)
+    _rows("quantize_fp8", x)
+    code = _DTYPE_CODE.get(str(x.dtype)[6:])
+    if code is None:
+        raise ValueError(f"quantize_fp8: {x.dtype} is not bf16, f16 or f32")
+    M, K = x.shape
+    with _allocating(stream):
+        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+        scales = torch.empty((-(-M // max(block_rows, 1)), -(-K // 128)), dtype=torch.float8_e8m0fnu, device=x.device)
+    _check(lib.asr_op_quantize_fp8(x.data_ptr(), code, x.stride(0), M, K, block_rows, codes.data_ptr(),
+                                   scales.data_ptr(), _stream(stream)))
+    return codes, scales
+
+
+def linear_fp8(x, x_scales, w, w_scales, bias=None, epi: int = EPI_BF16, out=None, workspace=None, stream=None):
+    """Quantised x [M, K] and w [N, K] (float8_e4m3fn codes, float8_e8m0fnu scales: quantize_fp8(x) and
+    quantize_fp8(w, 128)), bias f32 [N] -> epilogue(x w^T + bias) (asr_op_linear_fp8).  workspace: a zeroed
+    CUDA tensor of asr_op_linear_fp8_ws_size() bytes whose first int32 the call sets if a device wait gives up;
+    a program that calls this often keeps one."""
+    import torch
+    _operands("linear_fp8", x, x_scales, w, w_scales, bias, out, workspace)
+    M, K = x.shape
+    N = w.shape[0]
+    KB = -(-K // 128)
+    if not (x.dtype == w.dtype == torch.float8_e4m3fn and x_scales.dtype == w_scales.dtype == torch.float8_e8m0fnu):
+        raise ValueError("linear_fp8: codes must be float8_e4m3fn and scales float8_e8m0fnu")
+    if (w.shape[1] != K or tuple(x_scales.shape) != (M, KB) or tuple(w_scales.shape) != (-(-N // 128), KB) or not (
+            x.is_contiguous() and w.is_contiguous() and x_scales.is_contiguous() and w_scales.is_contiguous())):
+        raise ValueError("linear_fp8: need contiguous x [M, K], w [N, K], x_scales [M, ceil(K/128)] and "
+                         "w_scales [ceil(N/128), ceil(K/128)]")
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,) or not bias.is_contiguous()):
+        raise ValueError("linear_fp8: bias must be contiguous float32 [N]")
+    dt = torch.float32 if epi in (EPI_F32, EPI_F32_RESID) else torch.float16 if epi == EPI_F16 else torch.bfloat16
+    shape = (M, N // 2 if epi == EPI_SWIGLU else N)
+    with _allocating(stream):
+        if out is None:
+            if epi == EPI_F32_RESID:
+                raise ValueError("EPI_F32_RESID needs `out` (updated in place)")
+            out = torch.empty(shape, dtype=dt, device=x.device)
+        elif out.dtype != dt or tuple(out.shape) != shape or not out.is_contiguous():
+            raise ValueError(f"linear_fp8: out must be a contiguous {dt} tensor of shape {shape}")
+        if workspace is None:
+            workspace = torch.zeros(256, dtype=torch.uint8, device=x.device)
+    _check(lib.asr_op_linear_fp8(x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
+                                 None if bias is None else bias.data_ptr(), M, N, K, epi, out.data_ptr(),
+                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
 
 
 def wait_probe(limit_ns: int, stream=None) -> int:

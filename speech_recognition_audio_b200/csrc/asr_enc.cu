@@ -1856,6 +1856,62 @@ asr_status asr_splice_check(const void* ws, void* stream) {
   return ASR_OK;
 }
 
+asr_status asr_op_quantize_fp8(const void* x, int x_dtype, int64_t ldx, int64_t M, int K, int block_rows, void* codes,
+                               void* scales, void* stream) {
+  const int es = x_dtype == ASR_DTYPE_F32 ? 4 : 2;
+  if (!x || !codes || !scales || M <= 0 || K <= 0 || K % 16 || ldx < K || (ldx * es) % 16 ||
+      ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(codes)) & 15))
+    return fail(nullptr, ASR_E_INVAL, "quantize_fp8: bad arguments (K %% 16, rows and pointers of whole 16 bytes)");
+  if (x_dtype != ASR_DTYPE_BF16 && x_dtype != ASR_DTYPE_F16 && x_dtype != ASR_DTYPE_F32)
+    return fail(nullptr, ASR_E_INVAL, "quantize_fp8: unknown element type %d", x_dtype);
+  if (block_rows != 1 && block_rows != 128)
+    return fail(nullptr, ASR_E_INVAL, "quantize_fp8: block_rows must be 1 or 128");
+  if (M > 0x7FFFFFFF / ((K + 127) / 128)) return fail(nullptr, ASR_E_UNSUPPORTED, "quantize_fp8: too many blocks");
+  ASR_CUDA(nullptr, launch_quantize_fp8(x, x_dtype, ldx, M, K, block_rows, static_cast<uint8_t*>(codes),
+                                        static_cast<uint8_t*>(scales), static_cast<cudaStream_t>(stream)));
+  return ASR_OK;
+}
+
+size_t asr_op_linear_fp8_ws_size(void) { return 256; }
+
+asr_status asr_op_linear_fp8(const void* x, const void* xs, const void* w, const void* ws, const float* bias,
+                             int64_t M, int N, int K, int epi, void* y, void* scratch, size_t scratch_bytes,
+                             void* stream) {
+  if (!x || !xs || !w || !ws || !y || M <= 0 || N <= 0 || K <= 0 || K % 16 || N % 16 || M > 0x7FFFFF00)
+    return fail(nullptr, ASR_E_INVAL, "linear_fp8: bad arguments (K %% 16, N %% 16)");
+  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(y)) & 15)
+    return fail(nullptr, ASR_E_INVAL, "linear_fp8: operands must be 16-byte aligned");
+  if (!scratch || scratch_bytes < asr_op_linear_fp8_ws_size() || (reinterpret_cast<uintptr_t>(scratch) & 3))
+    return fail(nullptr, ASR_E_WORKSPACE, "linear_fp8: workspace too small");
+  int e_bits = 0;
+  switch (epi) {
+    case ASR_EPI_BF16:
+    case ASR_EPI_F16: break;
+    case ASR_EPI_BF16_GELU: e_bits = EPI_GELU; break;
+    case ASR_EPI_F32_RESID: e_bits = EPI_RESID; break;
+    case ASR_EPI_F32: e_bits = EPI_OUT_F32; break;
+    case ASR_EPI_SWIGLU:
+      if (N % 32) return fail(nullptr, ASR_E_INVAL, "linear_fp8: SwiGLU needs N %% 32 == 0");
+      e_bits = EPI_SWIGLU;
+      break;
+    default: return fail(nullptr, ASR_E_INVAL, "linear_fp8: unknown epilogue %d", epi);
+  }
+  GemmParams p;
+  memset(&p, 0, sizeof p);
+  p.M = (int)M;
+  p.N = N;
+  p.K = K;
+  p.out = y;
+  p.ldo = (e_bits & EPI_SWIGLU) ? N / 2 : N;
+  p.bias = bias;
+  p.pe_period = 1;
+  p.status = static_cast<int*>(scratch);
+  p.limit_ns = kWaitLimitNs;
+  ASR_CUDA(nullptr, launch_linear_fp8(x, static_cast<const uint8_t*>(xs), w, static_cast<const uint8_t*>(ws), p, e_bits,
+                                      epi == ASR_EPI_F16, current_sm_count(), static_cast<cudaStream_t>(stream)));
+  return ASR_OK;
+}
+
 asr_status asr_op_gelu(const float* x, float* y, int64_t n, void* stream) {
   if (!x || !y || n <= 0) return fail(nullptr, ASR_E_INVAL, "gelu: bad arguments");
   ASR_CUDA(nullptr, launch_gelu(x, y, n, static_cast<cudaStream_t>(stream)));

@@ -139,6 +139,13 @@ cudaError_t launch_splice(const int* ids, long long n_ids, int placeholder, cons
                           int table_dtype, const float* frames, long long n_frames, int D, void* out, int out_dtype,
                           int* rank, int* status, int num_sms, cudaStream_t st);
 
+// fp8 with block scales (fp8.cu).  x_dtype: SPLICE_*; block_rows 1 or 128.
+cudaError_t launch_quantize_fp8(const void* x, int x_dtype, long long ldx, long long M, int K, int block_rows,
+                                uint8_t* codes, uint8_t* scales, cudaStream_t st);
+// p: M, N, K, out, ldo, bias, status, limit_ns; epi: EPI_* bits; f16: 16-bit outputs are f16.
+cudaError_t launch_linear_fp8(const void* x, const uint8_t* xs, const void* w, const uint8_t* ws, GemmParams p, int epi,
+                              bool f16, int num_sms, cudaStream_t st);
+
 cudaError_t launch_fill_windows(int* cu, int batch, int tokens_per_clip, int window, int n_win_per_clip,
                                 cudaStream_t st);
 // 16-bit (bf16, or f16 with f16 != 0) to fp32.
@@ -167,6 +174,9 @@ bool make_tmap_bf16(CUtensorMap* map, const void* ptr, unsigned long long rows, 
 // fp32 activation map (box 32 x box_rows: one 128-byte row per box row).
 bool make_tmap_f32(CUtensorMap* map, const void* ptr, unsigned long long rows, unsigned long long cols,
                    unsigned long long row_stride_elems, unsigned int box_rows);
+// 8-bit operand map of contiguous rows (box 128 x box_rows; cols % 16 == 0).
+bool make_tmap_u8(CUtensorMap* map, const void* ptr, unsigned long long rows, unsigned long long cols,
+                  unsigned int box_rows);
 // A-operand map of an activation of the kind's element type.
 bool make_tmap_act(int kind, CUtensorMap* map, const void* ptr, unsigned long long rows, unsigned long long cols,
                    unsigned long long row_stride_elems, unsigned int box_rows);
