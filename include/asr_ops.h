@@ -194,6 +194,62 @@ asr_status asr_op_linear_fp8(const void* x, const void* xs, const void* w, const
                              int64_t M, int N, int K, int epi, void* y, void* scratch, size_t scratch_bytes,
                              void* stream);
 
+/* ---- cross attention ---------------------------------------------------------
+ * A decoder's tokens over the encoder states of their clip ("CrisperWhisper ->
+ * ONNX (with cross-attentions)", whisper-small decoder): for segment j, row i
+ * of [cu_q[j], cu_q[j+1]) and head h,
+ *   out[i, h] = softmax over the states n of [cu_k[j], cu_k[j+1]) of
+ *               (q[i, h] . k[n, h / G] / 8)  times  v[n, h / G],   G = H / Hkv.
+ * A segment without states gives rows of zeros; a segment without rows
+ * nothing; rows of `out` outside every segment are left as they were.
+ *  q     device [Tq, H * 64] of dtype (ASR_DTYPE_BF16 or ASR_DTYPE_F16), row
+ *        stride ldq elements; out likewise with ldo.  head_dim 64.
+ *  k, v  device [Tk, Hkv * 64] of the same type, row strides ldk, ldv: columns
+ *        of a wider matrix (one layer of a product over all layers' weights)
+ *        serve as they are.  Only a segment's own states are read for it, so
+ *        other rows may hold anything, NaN included.
+ *  cu_q, cu_k  device int32 [n_seg + 1], non-decreasing, within [0, Tq] / [0, Tk].
+ *  max_q  at least the longest segment's rows; max_k the longest segment's
+ *         states (it chooses how the work is split; any value >= 0 is right).
+ *  ws     device scratch of >= asr_op_cross_attention_ws_size() bytes whose
+ *         first int32 is the status word.  Zero it once before its first use:
+ *         a call sets the word when a segment's offsets leave the arrays or
+ *         exceed max_q (7; that segment's rows are not written) or a bounded
+ *         device wait gives up (other codes), and never clears it, so calls on
+ *         one stream or several may share it.  asr_op_cross_attention_check()
+ *         synchronises the stream and turns the word into ASR_OK, ASR_E_INVAL
+ *         or ASR_E_DEVICE_TIMEOUT.
+ * Limits: H % Hkv == 0, strides multiples of 8 elements and at least the row
+ * width, pointers 16-byte aligned (ASR_E_INVAL); Hkv <= 65535 and max_q * G <=
+ * 1048560 (ASR_E_UNSUPPORTED).  Tq == 0 does nothing.
+ * Results do not depend on timing: the parts of a split row are joined in a
+ * fixed order. */
+size_t asr_op_cross_attention_ws_size(void);
+asr_status asr_op_cross_attention(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                  const int32_t* cu_q, const int32_t* cu_k, int n_seg, int max_q, int max_k,
+                                  int64_t Tq, int64_t Tk, int H, int Hkv, int dtype, void* out, int64_t ldo, void* ws,
+                                  size_t ws_bytes, void* stream);
+asr_status asr_op_cross_attention_check(const void* ws, void* stream);
+
+/* The attention weights themselves, which word timestamps are read from
+ * (Results of the same page: a (1, 12, 1, 1500) tensor per token):
+ *   weights[s, i, n] = softmax over the segment's states of
+ *                      (q[i, heads[s]] . k[n, heads[s] / G] / 8)
+ * in fp32, n counted from the segment's first state.  Columns n from the
+ * segment's states to max_k are zero; rows outside every segment are left.
+ *  heads    device int32 [n_sel], the query heads wanted (a value outside
+ *           [0, H) sets the status word to 7 and writes nothing).
+ *  weights  device float32 [n_sel, Tq, ldw], ldw >= max_k (rows of whole 32
+ *           bytes, ldw % 8 == 0 and an aligned pointer, are written fastest);
+ *           columns from max_k to ldw are not touched.
+ *  max_k    at least the longest segment's states (a longer one sets the
+ *           status word to 7 and is not written).
+ * Everything else as for asr_op_cross_attention. */
+asr_status asr_op_cross_attention_weights(const void* q, int64_t ldq, const void* k, int64_t ldk, const int32_t* cu_q,
+                                          const int32_t* cu_k, int n_seg, int max_q, int max_k, int64_t Tq, int64_t Tk,
+                                          int H, int Hkv, int dtype, const int32_t* heads, int n_sel, float* weights,
+                                          int64_t ldw, void* ws, size_t ws_bytes, void* stream);
+
 /* Bounded-wait self-check: launches one kernel that waits on a shared-memory
  * barrier that nothing ever completes, gives up after limit_ns nanoseconds
  * of device time, writes 1 to *status_dev (device int32) and returns

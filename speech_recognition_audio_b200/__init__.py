@@ -15,6 +15,7 @@ The entry points mirror ``include/asr_enc.h`` and ``include/asr_ops.h``:
   log_mel, linear, layer_norm, attention,
   wait_probe                               kernel-level ops
   quantize_fp8, linear_fp8                 fp8 operands with a scale per block of 128
+  cross_attention, cross_attention_weights a decoder's tokens over the encoder states
   splice_embeddings                        asr_splice_embeddings / asr_splice_check
   Stream(encoder).push / finish            asr_stream_* (live input, window by window)
 """
@@ -25,7 +26,7 @@ import os
 
 __all__ = ["lib", "LIB_PATH", "AsrError", "Geometry", "tokens", "windows", "weight_names", "Encoder", "Stream",
            "log_mel", "linear", "linear_tf32", "layer_norm", "attention", "gelu", "wait_probe", "splice_embeddings",
-           "quantize_fp8", "linear_fp8", "TAP_MEL", "TAP_STEM",
+           "quantize_fp8", "linear_fp8", "cross_attention", "cross_attention_weights", "TAP_MEL", "TAP_STEM",
            "TAP_LAYER0", "TAP_ENCODER", "TAP_HEAD", "EPI_BF16", "EPI_BF16_GELU", "EPI_F32_RESID",
            "EPI_F32", "EPI_SWIGLU", "EPI_F16"]
 
@@ -106,6 +107,10 @@ def _load():
         "asr_op_quantize_fp8": (I, [P, I, I64, I64, I, I, P, P, P]),
         "asr_op_linear_fp8_ws_size": (SZ, []),
         "asr_op_linear_fp8": (I, [P, P, P, P, P, I64, I, I, I, P, P, SZ, P]),
+        "asr_op_cross_attention_ws_size": (SZ, []),
+        "asr_op_cross_attention": (I, [P, I64, P, I64, P, I64, P, P, I, I, I, I64, I64, I, I, I, P, I64, P, SZ, P]),
+        "asr_op_cross_attention_check": (I, [P, P]),
+        "asr_op_cross_attention_weights": (I, [P, I64, P, I64, P, P, I, I, I, I64, I64, I, I, I, P, I, P, I64, P, SZ, P]),
         "asr_op_wait_probe": (I, [I64, P, P]),
         "asr_stream_window_tokens": (I64, [P]),
         "asr_stream_workspace_size": (SZ, [P, I]),
@@ -540,6 +545,92 @@ def linear_fp8(x, x_scales, w, w_scales, bias=None, epi: int = EPI_BF16, out=Non
     _check(lib.asr_op_linear_fp8(x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
                                  None if bias is None else bias.data_ptr(), M, N, K, epi, out.data_ptr(),
                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+def _cross_operands(what, q, k, v, cu_q, cu_k, max_q, max_k, out, workspace):
+    """What the two cross-attention calls check alike -> (n_seg, max_q, max_k, H, Hkv)."""
+    import torch
+    _operands(what, q, k, v, cu_q, cu_k, out, workspace)
+    if q.dtype not in (torch.bfloat16, torch.float16) or k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+        raise ValueError(f"{what}: q, k and v must be of one type, bf16 or f16")
+    _rows(what, q)
+    _rows(what, k)
+    if v is not None:
+        _rows(what, v, k.shape[1])
+    if q.shape[1] % 64 or k.shape[1] % 64 or not q.shape[1] or not k.shape[1] or q.shape[1] % k.shape[1] or (
+            v is not None and v.shape[0] != k.shape[0]):
+        raise ValueError(f"{what}: need q [Tq, H * 64] and k, v [Tk, Hkv * 64] with H a multiple of Hkv")
+    n_seg = cu_q.numel() - 1
+    if cu_q.dtype != torch.int32 or cu_k.dtype != torch.int32 or cu_q.dim() != 1 or tuple(cu_q.shape) != tuple(
+            cu_k.shape) or n_seg < 1 or not cu_q.is_contiguous() or not cu_k.is_contiguous():
+        raise ValueError(f"{what}: cu_q and cu_k must be contiguous int32 [n_seg + 1]")
+    if max_q is None:
+        max_q = int((cu_q[1:] - cu_q[:-1]).max())
+    if max_k is None:
+        max_k = int((cu_k[1:] - cu_k[:-1]).max())
+    return n_seg, max_q, max_k, q.shape[1] // 64, k.shape[1] // 64
+
+
+def cross_attention(q, k, v, cu_q, cu_k, max_q=None, max_k=None, out=None, workspace=None, stream=None,
+                    check: bool = True):
+    """q CUDA [Tq, H*64], k and v CUDA [Tk, Hkv*64] (bf16 or f16, rows may be strided: a layer's columns of a
+    product over all layers), cu_q / cu_k int32 CUDA [n_seg+1] -> [Tq, H*64] (asr_op_cross_attention).  Without
+    max_q / max_k they are read from the device (a synchronisation).  Rows outside every segment are not
+    written (out keeps what it held).  workspace: a zeroed CUDA tensor of
+    asr_op_cross_attention_ws_size() bytes; with check the call synchronises and raises on bad offsets."""
+    import torch
+    n_seg, max_q, max_k, H, Hkv = _cross_operands("cross_attention", q, k, v, cu_q, cu_k, max_q, max_k, out, workspace)
+    with _allocating(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif out.dtype != q.dtype or out.shape != q.shape or (out.stride(1) != 1 and out.shape[1] > 1):
+            raise ValueError("cross_attention: out must be like q")
+        if workspace is None:
+            workspace = torch.zeros(256, dtype=torch.uint8, device=q.device)
+    st = _stream(stream)
+    _check(lib.asr_op_cross_attention(q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
+                                      cu_q.data_ptr(), cu_k.data_ptr(), n_seg, max_q, max_k, q.shape[0], k.shape[0], H,
+                                      Hkv, 2 if q.dtype == torch.float16 else 0, out.data_ptr(), out.stride(0),
+                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(), st))
+    if check:
+        _check(lib.asr_op_cross_attention_check(workspace.data_ptr(), st))
+    return out
+
+
+def cross_attention_weights(q, k, cu_q, cu_k, max_q=None, max_k=None, heads=None, out=None, workspace=None,
+                            stream=None, check: bool = True):
+    """Attention weights of the listed query heads (int32 CUDA tensor; default all): float32
+    [len(heads), Tq, max_k], columns past a segment's states zero (asr_op_cross_attention_weights).  out: such a
+    tensor with contiguous columns and equally spaced rows; else the result is a view of rows padded to whole
+    32 bytes."""
+    import torch
+    n_seg, max_q, max_k, H, Hkv = _cross_operands("cross_attention_weights", q, k, None, cu_q, cu_k, max_q, max_k, out,
+                                                  workspace)
+    Tq = q.shape[0]
+    with _allocating(stream):
+        if heads is None:
+            heads = torch.arange(H, dtype=torch.int32, device=q.device)
+        _operands("cross_attention_weights", heads)
+        if heads.dtype != torch.int32 or heads.dim() != 1 or not heads.is_contiguous():
+            raise ValueError("cross_attention_weights: heads must be a contiguous int32 vector")
+        n = heads.numel()
+        if out is None:
+            ldw = -(-max_k // 8) * 8
+            out = torch.empty((n, Tq, ldw), dtype=torch.float32, device=q.device)[:, :, :max_k]
+        elif out.dtype != torch.float32 or tuple(out.shape) != (n, Tq, max_k) or (out.stride(2) != 1 and max_k > 1) or (
+                n > 1 and out.stride(0) != Tq * out.stride(1)):
+            raise ValueError("cross_attention_weights: out must be float32 [len(heads), Tq, max_k] with equally spaced rows")
+        if workspace is None:
+            workspace = torch.zeros(256, dtype=torch.uint8, device=q.device)
+    st = _stream(stream)
+    _check(lib.asr_op_cross_attention_weights(q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0), cu_q.data_ptr(),
+                                              cu_k.data_ptr(), n_seg, max_q, max_k, Tq, k.shape[0], H, Hkv,
+                                              2 if q.dtype == torch.float16 else 0, heads.data_ptr(), n, out.data_ptr(),
+                                              out.stride(1), workspace.data_ptr(),
+                                              workspace.numel() * workspace.element_size(), st))
+    if check:
+        _check(lib.asr_op_cross_attention_check(workspace.data_ptr(), st))
     return out
 
 

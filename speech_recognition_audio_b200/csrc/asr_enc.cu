@@ -1912,6 +1912,87 @@ asr_status asr_op_linear_fp8(const void* x, const void* xs, const void* w, const
   return ASR_OK;
 }
 
+size_t asr_op_cross_attention_ws_size(void) { return 256; }
+
+// What the two cross-attention entry points check alike; fills `a`.
+static asr_status xattn_args(const char* who, XattnArgs& a, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                             const void* v, int64_t ldv, const int32_t* cu_q, const int32_t* cu_k, int n_seg, int max_q,
+                             int max_k, int64_t Tq, int64_t Tk, int H, int Hkv, int dtype, void* out, int64_t ldo,
+                             void* ws, size_t ws_bytes) {
+  if (dtype != ASR_DTYPE_BF16 && dtype != ASR_DTYPE_F16)
+    return fail(nullptr, dtype == ASR_DTYPE_F32 ? ASR_E_UNSUPPORTED : ASR_E_INVAL, "%s: dtype must be bf16 or f16", who);
+  if (Tq < 0 || Tk < 0 || n_seg <= 0 || max_q < 0 || max_k < 0 || H <= 0 || Hkv <= 0 || H % Hkv || !cu_q || !cu_k)
+    return fail(nullptr, ASR_E_INVAL, "%s: bad arguments", who);
+  if (!ws || ws_bytes < asr_op_cross_attention_ws_size() || (reinterpret_cast<uintptr_t>(ws) & 3))
+    return fail(nullptr, ASR_E_WORKSPACE, "%s: workspace too small", who);
+  if (Tq > 0x7FFFFFFF || Tk > 0x7FFFFFFF || Hkv > 65535 || n_seg > 0x7FFFFFFF / 8 ||
+      (long long)max_q * (H / Hkv) > 16LL * 65535)
+    return fail(nullptr, ASR_E_UNSUPPORTED, "%s: sizes beyond the limits", who);
+  const int64_t wq = 64LL * H, wk = 64LL * Hkv;
+  if (Tq > 0 && (!q || !out || (reinterpret_cast<uintptr_t>(q) & 15) || ldq < wq || ldq % 8))
+    return fail(nullptr, ASR_E_INVAL, "%s: q must have aligned rows of H * 64 elements", who);
+  if (Tk > 0 && (!k || (reinterpret_cast<uintptr_t>(k) & 15) || ldk < wk || ldk % 8 || (reinterpret_cast<uintptr_t>(v) & 15) ||
+                 (v && (ldv < wk || ldv % 8))))
+    return fail(nullptr, ASR_E_INVAL, "%s: k and v must have aligned rows of Hkv * 64 elements", who);
+  memset(&a, 0, sizeof a);
+  a.q = q, a.k = k, a.v = v;
+  a.ldq = ldq, a.ldk = ldk, a.ldv = ldv, a.ldo = ldo;
+  a.cu_q = cu_q, a.cu_k = cu_k;
+  a.Tq = Tq, a.Tk = Tk;
+  a.max_q = max_q, a.H = H, a.G = H / Hkv;
+  a.out = out;
+  a.status = static_cast<int*>(ws);
+  a.limit_ns = kWaitLimitNs;
+  return ASR_OK;
+}
+
+asr_status asr_op_cross_attention(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                  const int32_t* cu_q, const int32_t* cu_k, int n_seg, int max_q, int max_k, int64_t Tq,
+                                  int64_t Tk, int H, int Hkv, int dtype, void* out, int64_t ldo, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  XattnArgs a;
+  const asr_status r = xattn_args("cross_attention", a, q, ldq, k, ldk, v, ldv, cu_q, cu_k, n_seg, max_q, max_k, Tq, Tk,
+                                  H, Hkv, dtype, out, ldo, ws, ws_bytes);
+  if (r != ASR_OK) return r;
+  if ((Tk > 0 && !v) || (Tq > 0 && ((reinterpret_cast<uintptr_t>(out) & 15) || ldo < 64LL * H || ldo % 8)))
+    return fail(nullptr, ASR_E_INVAL, "cross_attention: out must have aligned rows of H * 64 elements, and v be given");
+  if (Tq == 0 || max_q == 0) return ASR_OK;
+  ASR_CUDA(nullptr, launch_xattn(a, n_seg, max_k, dtype == ASR_DTYPE_F16, current_sm_count(),
+                                 static_cast<cudaStream_t>(stream)));
+  return ASR_OK;
+}
+
+asr_status asr_op_cross_attention_check(const void* ws, void* stream) {
+  if (!ws) return fail(nullptr, ASR_E_INVAL, "cross_attention_check: workspace is NULL");
+  int code = 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ASR_CUDA(nullptr, cudaMemcpyAsync(&code, ws, 4, cudaMemcpyDeviceToHost, st));
+  ASR_CUDA(nullptr, cudaStreamSynchronize(st));
+  if (code == DEV_OK) return ASR_OK;
+  if (code == DEV_BAD_SEGMENT)
+    return fail(nullptr, ASR_E_INVAL, "cross_attention: segment offsets outside the arrays or longer than max_q / max_k, "
+                                      "or a head outside [0, H)");
+  return fail(nullptr, ASR_E_DEVICE_TIMEOUT, "cross_attention: a bounded device wait gave up (code %d)", code);
+}
+
+asr_status asr_op_cross_attention_weights(const void* q, int64_t ldq, const void* k, int64_t ldk, const int32_t* cu_q,
+                                          const int32_t* cu_k, int n_seg, int max_q, int max_k, int64_t Tq, int64_t Tk,
+                                          int H, int Hkv, int dtype, const int32_t* heads, int n_sel, float* weights,
+                                          int64_t ldw, void* ws, size_t ws_bytes, void* stream) {
+  XattnArgs a;
+  const asr_status r = xattn_args("cross_attention_weights", a, q, ldq, k, ldk, nullptr, 0, cu_q, cu_k, n_seg, max_q,
+                                  max_k, Tq, Tk, H, Hkv, dtype, weights, ldw, ws, ws_bytes);
+  if (r != ASR_OK) return r;
+  if (!heads || n_sel <= 0 || n_sel > 65535 || ldw < max_k || (reinterpret_cast<uintptr_t>(weights) & 3))
+    return fail(nullptr, ASR_E_INVAL, "cross_attention_weights: need heads and ldw >= max_k");
+  if (Tq == 0 || max_q == 0 || max_k == 0) return ASR_OK;
+  a.heads = heads;
+  a.width = max_k;
+  ASR_CUDA(nullptr, launch_xattn_weights(a, n_seg, n_sel, dtype == ASR_DTYPE_F16, current_sm_count(),
+                                         static_cast<cudaStream_t>(stream)));
+  return ASR_OK;
+}
+
 asr_status asr_op_gelu(const float* x, float* y, int64_t n, void* stream) {
   if (!x || !y || n <= 0) return fail(nullptr, ASR_E_INVAL, "gelu: bad arguments");
   ASR_CUDA(nullptr, launch_gelu(x, y, n, static_cast<cudaStream_t>(stream)));

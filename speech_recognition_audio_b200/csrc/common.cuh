@@ -14,7 +14,8 @@ typedef __nv_bfloat16 bf16;
 
 // Device status codes written to the forward's status word.
 enum : int { DEV_OK = 0, DEV_TIMEOUT_PRODUCER = 1, DEV_TIMEOUT_MMA = 2, DEV_TIMEOUT_EPILOGUE = 3,
-             DEV_TIMEOUT_GATHER = 4, DEV_TIMEOUT_DRAIN = 5, DEV_TIMEOUT_PROBE = 6 };
+             DEV_TIMEOUT_GATHER = 4, DEV_TIMEOUT_DRAIN = 5, DEV_TIMEOUT_PROBE = 6,
+             DEV_BAD_SEGMENT = 7 };  // segment offsets outside the arrays, or longer than stated
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -139,6 +139,23 @@ cudaError_t launch_splice(const int* ids, long long n_ids, int placeholder, cons
                           int table_dtype, const float* frames, long long n_frames, int D, void* out, int out_dtype,
                           int* rank, int* status, int num_sms, cudaStream_t st);
 
+// Cross attention and its weights (xattn.cu).
+struct XattnArgs {
+  const void *q, *k, *v;       // 16-bit rows; v null for the weights
+  long long ldq, ldk, ldv, ldo;  // row strides in elements
+  const int *cu_q, *cu_k;      // [n_seg + 1] offsets of the segments' rows and states
+  const int* heads;            // weights: the selected heads
+  long long Tq, Tk;            // rows of q and of k / v
+  int max_q, H, G;             // longest segment of rows, query heads, query heads per key head
+  int width;                   // weights: columns of a row (0 for the attention)
+  void* out;
+  int* status;
+  int splits;                  // set by the launcher
+  unsigned long long limit_ns;
+};
+cudaError_t launch_xattn(XattnArgs a, int n_seg, int max_k, bool f16, int num_sms, cudaStream_t st);
+cudaError_t launch_xattn_weights(XattnArgs a, int n_seg, int n_sel, bool f16, int num_sms, cudaStream_t st);
+
 // fp8 with block scales (fp8.cu).  x_dtype: SPLICE_*; block_rows 1 or 128.
 cudaError_t launch_quantize_fp8(const void* x, int x_dtype, long long ldx, long long M, int K, int block_rows,
                                 uint8_t* codes, uint8_t* scales, cudaStream_t st);
