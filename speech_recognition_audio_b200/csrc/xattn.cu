@@ -20,34 +20,11 @@
 // fragments follow the same order, and the values' columns are permuted the
 // same way.  mma.sync rather than tcgen05: a 128-row tile would be all but
 // empty, and the tensor pipe is idle most of the time either way.
-#include "gemm2.cuh"
-#include "kernels.h"
+#include "xattn.cuh"
 
 namespace asr {
 
 namespace {
-
-constexpr float kScaleLog2 = 0.125f * 1.4426950408889634f;  // log2(e) / sqrt(64)
-
-struct Segment {
-  int q0, lq, k0, lk;
-  bool ok;
-};
-
-// Rows and states of segment `seg`; not ok (and reported) when its offsets
-// leave the arrays or it is longer than the caller said.
-__device__ __forceinline__ Segment load_segment(const XattnArgs& a, int seg, bool report) {
-  Segment s;
-  s.q0 = __ldg(a.cu_q + seg);
-  s.k0 = __ldg(a.cu_k + seg);
-  const int q1 = __ldg(a.cu_q + seg + 1), k1 = __ldg(a.cu_k + seg + 1);
-  s.lq = q1 - s.q0;
-  s.lk = k1 - s.k0;
-  s.ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= a.Tq && s.k0 >= 0 && k1 >= s.k0 && k1 <= a.Tk && s.lq <= a.max_q &&
-         (a.width == 0 || s.lk <= a.width);
-  if (!s.ok && report) atomicCAS(a.status, 0, DEV_BAD_SEGMENT);
-  return s;
-}
 
 template <int KIND>
 __device__ __forceinline__ void mma16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -66,20 +43,6 @@ __device__ __forceinline__ void mma16(float* c, const uint32_t* a, uint32_t b0, 
 __device__ __forceinline__ uint4 ld16(const uint16_t* p, bool valid) {
   return valid ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
 // Query fragments of 16 rows (row r of the tile: token r / G, head kvh G + r % G):
 // lane (g, t) holds, of rows g and g + 8, elements 8 t .. 8 t + 7 and
 // 32 + 8 t .. 32 + 8 t + 7, i.e. k step s is elements 32 (s / 2) + 8 t + 4 (s % 2) + 0..3.
@@ -110,10 +73,6 @@ __device__ __forceinline__ void scores8(float* c, const uint32_t (*qf)[4], const
   mma16<KIND>(c, qf[2], hi.x, hi.y);
   mma16<KIND>(c, qf[3], hi.z, hi.w);
 }
-
-// Maximum to subtract: 0 where no score is above -inf, so that
-// exp(-inf - m) is 0 there and not NaN.
-__device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.f : m; }
 
 constexpr int XS_WARPS = 4, XS_KEYS = 32;  // warps of a block, keys of a warp's step
 
@@ -434,42 +393,13 @@ __global__ void __launch_bounds__(32 * XW_WARPS, 2) xattn_weights_kernel(const X
   }
 }
 
-namespace {
-
-template <typename Kernel>
-cudaError_t launch_split(Kernel k, dim3 grid, int threads, int splits, cudaStream_t st, const XattnArgs& a) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = splits;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k, a);
-}
-
-// Blocks a (segment, tile, head) is split into: a power of two up to the
-// portable cluster size, while the grid does not yet fill `fill` blocks and
-// each block keeps at least `least` keys.
-int pick_splits(long long blocks, int keys, int least, long long fill) {
-  int s = 1;
-  while (s < 8 && blocks * s < fill && keys >= 2 * s * least) s *= 2;
-  return s;
-}
-
-}  // namespace
-
 cudaError_t launch_xattn(XattnArgs a, int n_seg, int max_k, bool f16, int num_sms, cudaStream_t st) {
+  if (a.max_q > 32 && a.Tk > 0) return launch_xattn_tiles(a, n_seg, max_k, f16, num_sms, st);
   const int tiles = (int)(((long long)a.max_q * a.G + 15) / 16), Hkv = a.H / a.G;
   a.splits = pick_splits((long long)n_seg * tiles * Hkv, max_k, XS_WARPS * XS_KEYS, 2LL * num_sms);
   const dim3 grid(n_seg * a.splits, tiles, Hkv);
-  return f16 ? launch_split(xattn_rows_kernel<KIND_F16>, grid, 32 * XS_WARPS, a.splits, st, a)
-             : launch_split(xattn_rows_kernel<KIND_BF16>, grid, 32 * XS_WARPS, a.splits, st, a);
+  return f16 ? launch_split(xattn_rows_kernel<KIND_F16>, grid, 32 * XS_WARPS, 0, a.splits, st, a)
+             : launch_split(xattn_rows_kernel<KIND_BF16>, grid, 32 * XS_WARPS, 0, a.splits, st, a);
 }
 
 cudaError_t launch_xattn_weights(XattnArgs a, int n_seg, int n_sel, bool f16, int num_sms, cudaStream_t st) {
@@ -478,10 +408,10 @@ cudaError_t launch_xattn_weights(XattnArgs a, int n_seg, int n_sel, bool f16, in
   a.splits = pick_splits((long long)n_seg * tiles * n_sel, a.width, XW_WARPS * XW_KEYS, num_sms);
   const dim3 grid(n_seg * a.splits, tiles, n_sel);
   if (wide)
-    return f16 ? launch_split(xattn_weights_kernel<KIND_F16, 4>, grid, 32 * XW_WARPS, a.splits, st, a)
-               : launch_split(xattn_weights_kernel<KIND_BF16, 4>, grid, 32 * XW_WARPS, a.splits, st, a);
-  return f16 ? launch_split(xattn_weights_kernel<KIND_F16, 1>, grid, 32 * XW_WARPS, a.splits, st, a)
-             : launch_split(xattn_weights_kernel<KIND_BF16, 1>, grid, 32 * XW_WARPS, a.splits, st, a);
+    return f16 ? launch_split(xattn_weights_kernel<KIND_F16, 4>, grid, 32 * XW_WARPS, 0, a.splits, st, a)
+               : launch_split(xattn_weights_kernel<KIND_BF16, 4>, grid, 32 * XW_WARPS, 0, a.splits, st, a);
+  return f16 ? launch_split(xattn_weights_kernel<KIND_F16, 1>, grid, 32 * XW_WARPS, 0, a.splits, st, a)
+             : launch_split(xattn_weights_kernel<KIND_BF16, 1>, grid, 32 * XW_WARPS, 0, a.splits, st, a);
 }
 
 }  // namespace asr

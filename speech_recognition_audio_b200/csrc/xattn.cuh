@@ -1,0 +1,77 @@
+// Shared by the cross-attention kernels: segment bounds, distributed shared
+// memory reads, and the launch of a grid whose clusters split the keys.
+#pragma once
+
+#include "gemm2.cuh"
+#include "kernels.h"
+
+namespace asr {
+
+constexpr float kScaleLog2 = 0.125f * 1.4426950408889634f;  // log2(e) / sqrt(64)
+
+struct Segment {
+  int q0, lq, k0, lk;
+  bool ok;
+};
+
+// Rows and states of segment `seg`; not ok (and reported) when its offsets
+// leave the arrays or it is longer than the caller said.
+__device__ __forceinline__ Segment load_segment(const XattnArgs& a, int seg, bool report) {
+  Segment s;
+  s.q0 = __ldg(a.cu_q + seg);
+  s.k0 = __ldg(a.cu_k + seg);
+  const int q1 = __ldg(a.cu_q + seg + 1), k1 = __ldg(a.cu_k + seg + 1);
+  s.lq = q1 - s.q0;
+  s.lk = k1 - s.k0;
+  s.ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= a.Tq && s.k0 >= 0 && k1 >= s.k0 && k1 <= a.Tk && s.lq <= a.max_q &&
+         (a.width == 0 || s.lk <= a.width);
+  if (!s.ok && report) atomicCAS(a.status, 0, DEV_BAD_SEGMENT);
+  return s;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Maximum to subtract: 0 where no score is above -inf, so that
+// exp(-inf - m) is 0 there and not NaN.
+__device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_split(void (*k)(KArgs...), dim3 grid, int threads, size_t smem, int splits, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k, std::forward<Args>(args)...);
+}
+
+// Blocks a (segment, tile, head) is split into: a power of two up to the
+// portable cluster size, while the grid does not yet fill `fill` blocks and
+// each block keeps at least `least` keys.
+inline int pick_splits(long long blocks, int keys, int least, long long fill) {
+  int s = 1;
+  while (s < 8 && blocks * s < fill && keys >= 2 * s * least) s *= 2;
+  return s;
+}
+
+}  // namespace asr
