@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(Fp8Shape<BN>::THREADS, 1)
         tile_coords(p, t, mb, nb);
         for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
           const int s = it % STAGES;
-          if (!(ok = mbar_wait_bounded(&empty[s], ((it / STAGES) & 1) ^ 1, p.limit_ns, &failed, DEV_TIMEOUT_PRODUCER)))
+          if (!(ok = mbar_wait(&empty[s], ((it / STAGES) & 1) ^ 1, p.limit_ns, &failed, DEV_TIMEOUT_PRODUCER)))
             break;
           mbar_arrive_expect_tx(&full[s], S::STAGE_BYTES);
           tma_load_2d(sA + s * S::A_BYTES, &tmA, &full[s], kb * S::BK, mb * S::BM);
@@ -343,14 +343,14 @@ __global__ void __launch_bounds__(Fp8Shape<BN>::THREADS, 1)
       bool ok = true;
       for (int t = blockIdx.x; t < p.num_tiles && ok; t += gridDim.x, ++tl) {
         const int a = tl & 1;
-        if (!(ok = mbar_wait_bounded(&tempty[a], ((tl >> 1) & 1) ^ 1, p.limit_ns, &failed, DEV_TIMEOUT_MMA))) break;
+        if (!(ok = mbar_wait(&tempty[a], ((tl >> 1) & 1) ^ 1, p.limit_ns, &failed, DEV_TIMEOUT_MMA))) break;
         const uint32_t d = tmem + a * S::ACC_COLS;
         for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
           const int s = it % STAGES, slot = sg % S::SF_SLOTS;
-          if ((kb & 3) == 0 && !(ok = mbar_wait_bounded(&sfull[slot], (sg / S::SF_SLOTS) & 1, p.limit_ns, &failed,
+          if ((kb & 3) == 0 && !(ok = mbar_wait(&sfull[slot], (sg / S::SF_SLOTS) & 1, p.limit_ns, &failed,
                                                         DEV_TIMEOUT_MMA)))
             break;
-          if (!(ok = mbar_wait_bounded(&full[s], (it / STAGES) & 1, p.limit_ns, &failed, DEV_TIMEOUT_MMA))) break;
+          if (!(ok = mbar_wait(&full[s], (it / STAGES) & 1, p.limit_ns, &failed, DEV_TIMEOUT_MMA))) break;
           tc_fence_after();
           const uint64_t ad = sw128_kmajor_desc(smem_u32(sA + s * S::A_BYTES));
           const uint64_t bd = sw128_kmajor_desc(smem_u32(sB + s * S::B_BYTES));
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(Fp8Shape<BN>::THREADS, 1)
       tile_coords(p, t, mb, nb);
       float breg[4];
       load_bias(p, nb * BN, BN, half, lane, breg);
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[a], (tl >> 1) & 1, p.limit_ns, &failed, DEV_TIMEOUT_EPILOGUE)))
+      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[a], (tl >> 1) & 1, p.limit_ns, &failed, DEV_TIMEOUT_EPILOGUE)))
         break;
       tc_fence_after();
       const int m0 = mb * S::BM;
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(Fp8Shape<BN>::THREADS, 1)
           const int n = nb * BN + 32 * c + lane;
           w[S::SF_A + c] = sf_word(f.ws + (long long)(n >> 7) * f.KB, g, f.KB, n < p.N, word_ok);
         }
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sempty[slot], ((sg / S::SF_SLOTS) & 1) ^ 1, p.limit_ns,
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sempty[slot], ((sg / S::SF_SLOTS) & 1) ^ 1, p.limit_ns,
                                                              &failed, DEV_TIMEOUT_GATHER))))
           break;
         tc_fence_after();
