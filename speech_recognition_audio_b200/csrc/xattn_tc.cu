@@ -35,7 +35,11 @@ namespace asr {
 namespace {
 
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int XT_THREADS = 320, XT_TMA_WARP = 8, XT_MMA_WARP = 9;
+// whole warpgroups, so that registers can move from the load and issue warps
+// to the softmax; the sum stays within the launch's 384 x 80 (two blocks per SM)
+constexpr int XT_THREADS = 384, XT_TMA_WARP = 8, XT_MMA_WARP = 9;
+constexpr int XT_REGS_ISSUE = 32, XT_REGS_SOFTMAX = 104;
+static_assert(128 * XT_REGS_ISSUE + 256 * XT_REGS_SOFTMAX <= XT_THREADS * 80, "registers");
 // K and V tiles in flight (two blocks per SM leave 113 KB each)
 constexpr int XT_KS = 3, XT_VS = 2, XT_TILE = 16384;
 constexpr int XT_SQ = 0, XT_SK = XT_TILE, XT_SV = XT_SK + XT_KS * XT_TILE, XT_RED = XT_SV + XT_VS * XT_TILE;
@@ -129,9 +133,10 @@ __global__ void __launch_bounds__(XT_THREADS, 2)
   const int tiles = (s.lk + 127) / 128;
   const int t0 = (int)((long long)rank * tiles / S), nk = (int)((long long)(rank + 1) * tiles / S) - t0;
 
-  if (!live) {
-  } else if (warp >= XT_TMA_WARP) {
-    if (nk > 0 && warp == XT_TMA_WARP) {
+  if (warp >= XT_TMA_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(XT_REGS_ISSUE));
+    if (!live) {
+    } else if (nk > 0 && warp == XT_TMA_WARP) {
       if (lane == 0) {
         const int k0 = s.k0 + t0 * 128;
         mbar_arrive_expect_tx(&bar[XB_Q], XT_TILE);
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(XT_THREADS, 2)
         for (int j = max(0, nvl - XT_VS); j < nvl; ++j)
           mbar_wait(&bar[XB_VF + j % XT_VS], (j / XT_VS) & 1, kDrainLimitNs, nullptr, 0);
       }
-    } else if (nk > 0) {
+    } else if (nk > 0 && warp == XT_MMA_WARP) {
       const uint32_t idesc_s = idesc_kind_f32(KIND, 128, 128);
       const uint32_t idesc_o = idesc_kind_f32(KIND, 128, 64) | (1u << 16);  // B = V, MN-major
       const uint64_t qd = sw128_kmajor_desc(smem_u32(sm + XT_SQ)), kd = sw128_kmajor_desc(smem_u32(sm + XT_SK));
@@ -189,13 +194,15 @@ __global__ void __launch_bounds__(XT_THREADS, 2)
       tc_commit_warp(&bar[XB_DRAIN]);
       mbar_wait(&bar[XB_DRAIN], 0, kDrainLimitNs, nullptr, 0);
     }
-    if (S > 1) {  // the softmax warps' side of these is below
+    if (S > 1 && live) {  // the softmax warps' side of these is below
       __syncwarp();
       block_sync();
       cluster_sync();
       cluster_sync();
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(XT_REGS_SOFTMAX));
+    if (live) {
     const int q = warp & 3, hh = warp >> 2, row = 32 * q + lane;  // lane quarter, half of the states and of O
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * q) << 16);
     float m_used = -INFINITY, lsum = 0.f;  // the row's maximum, this half's sum
@@ -203,7 +210,7 @@ __global__ void __launch_bounds__(XT_THREADS, 2)
     // warps of a pair always meet the same barriers.
     bool ok = true;
     auto wait = [&](int b, int n) {
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(&bar[b], n & 1, a.limit_ns, &failed, DEV_TIMEOUT_EPILOGUE)) != 0;
+      ok = ok && mbar_wait(&bar[b], n & 1, a.limit_ns, &failed, DEV_TIMEOUT_EPILOGUE);
       tc_fence_after();
     };
     for (int j = 0; j < nk; ++j) {
@@ -229,23 +236,59 @@ __global__ void __launch_bounds__(XT_THREADS, 2)
           fence_proxy_async_smem();
         }
       }
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 64; c += 8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], fmaxf(sv[c + 2 * i], sv[c + 2 * i + 1]));
-      }
-      // buffers alternate: a warp writes one again only after its partner has
-      // passed the next barrier, having read it
+      // The row's maximum over both halves (scaled).  Buffers alternate: a warp
+      // writes one again only after its partner has passed the next barrier,
+      // having read it.
       float* rbuf = red + (j & 1) * 256;
-      rbuf[hh * 128 + row] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      pair_sync(q);
-      const float mt = fmaxf(rbuf[row], rbuf[128 + row]) * kScaleLog2;
+      auto row_max = [&](float mine) {
+        rbuf[hh * 128 + row] = mine;
+        pair_sync(q);
+        return fmaxf(rbuf[row], rbuf[128 + row]) * kScaleLog2;
+      };
+      // P = 2^(S scale - shift) into tensor memory; this half's sum, and its
+      // maximum formed beside the exponentials (each fills the other's waits)
+      float hm, sum;
+      auto exponentials = [&](bool wait_free) {
+        const float sh = shift_of(m_used);
+        const float2 scale2 = make_float2(kScaleLog2, kScaleLog2), shift2 = make_float2(-sh, -sh);
+        float2 s2[2] = {{0.f, 0.f}, {0.f, 0.f}};
+        float m2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          float pk[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 v = make_float2(sv[c + i], sv[c + i + 1]);
+            const float2 x = fma2(v, scale2, shift2);
+            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            m2[(i >> 1) & 1] = fmaxf(m2[(i >> 1) & 1], fmaxf(v.x, v.y));
+            s2[(i >> 1) & 1] = add2(s2[(i >> 1) & 1], p);
+            pk[i >> 1] = __uint_as_float(pack2_16<KIND>(p.x, p.y));
+          }
+          if (c == 0 && wait_free) wait(XB_OD, j - 1);  // P and O are free once the previous product is complete
+          tmem_st16(trow + XT_P + 32 * hh + c / 2, pk);
+        }
+        hm = fmaxf(m2[0], m2[1]);
+        sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+      };
+      // Past the first tile the exponentials go ahead with the maximum so far.
+      float mt;
+      if (j == 0) {
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 64; ++c) m4[c & 3] = fmaxf(m4[c & 3], sv[c]);
+        m_used = mt = row_max(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+        exponentials(false);
+      } else {
+        exponentials(true);
+        mt = row_max(hm);
+      }
       const bool grow = mt > m_used + kRescaleLog2;
-      const float corr = grow ? ex2_approx(m_used - mt) : 1.0f;  // 0 where there was no maximum yet
-      if (grow) m_used = mt;
-      if (j > 0 && __any_sync(0xffffffffu, grow)) {
-        wait(XB_OD, j - 1);  // O is still once the previous product is complete
+      if (__any_sync(0xffffffffu, grow)) {
+        // a row's maximum moved: O and the sum are rescaled, the tile's
+        // exponentials taken again
+        const float corr = grow ? ex2_approx(m_used - mt) : 1.0f;  // 0 where there was no maximum yet
+        if (grow) m_used = mt;
         lsum *= corr;
 #pragma unroll
         for (int c = 0; c < 32; c += 16) {
@@ -256,24 +299,9 @@ __global__ void __launch_bounds__(XT_THREADS, 2)
           for (int i = 0; i < 16; ++i) ov[i] *= corr;
           tmem_st16(trow + XT_O + 32 * hh + c, ov);
         }
+        exponentials(false);
       }
-      const float sh = shift_of(m_used);
-      const float2 scale2 = make_float2(kScaleLog2, kScaleLog2), shift2 = make_float2(-sh, -sh);
-      float2 s2[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        float pk[16];
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float2 x = fma2(make_float2(sv[c + i], sv[c + i + 1]), scale2, shift2);
-          const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-          s2[(i >> 1) & 3] = add2(s2[(i >> 1) & 3], p);
-          pk[i >> 1] = __uint_as_float(pack2_16<KIND>(p.x, p.y));
-        }
-        if (c == 0 && j > 0) wait(XB_OD, j - 1);  // P is free once the previous product has read it
-        tmem_st16(trow + XT_P + 32 * hh + c / 2, pk);
-      }
-      lsum += ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y));
+      lsum += sum;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -337,6 +365,7 @@ __global__ void __launch_bounds__(XT_THREADS, 2)
         for (int i = 0; i < 8; ++i) o8[i] = ov[8 * c + i] * inv;
         dst[c] = pack8_16<KIND>(o8);
       }
+    }
     }
   }
   tc_fence_before();
