@@ -23,42 +23,82 @@ namespace {
 constexpr int QZ_THREADS = 256;
 constexpr int QZ_UNROLL = 4;  // blocks of 128 in flight per half-warp
 
-// Eight consecutive elements as fp32 (16-byte loads; the pointer is aligned).
+// Eight consecutive elements as they are in memory: 16-byte loads (the
+// pointer is aligned), two for fp32.
 template <int DT>
-__device__ __forceinline__ void load8(const void* x, long long i, float* v) {
-  if constexpr (DT == SPLICE_F32) {
-    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(x) + i);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(x) + i));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw8 {
+  static constexpr int W = DT == SPLICE_F32 ? 8 : 4;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const void* x, long long i) {
+    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(x) + i * (DT == SPLICE_F32 ? 4 : 2));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (DT == SPLICE_BF16) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    for (int j = 0; j < W / 4; ++j) {
+      const uint4 u = __ldg(p + j);
+      w[4 * j] = u.x, w[4 * j + 1] = u.y, w[4 * j + 2] = u.z, w[4 * j + 3] = u.w;
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j] = 0;
+  }
+  // Largest magnitude as bits of the type, which order like the value
+  // (infinities and NaN above all): one word for fp32, the larger of each half
+  // of the words for the 16-bit types.
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      m = DT == SPLICE_F32 ? max(m, w[j] & 0x7FFFFFFFu) : __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+    return m;
+  }
+  // The same over the finite elements only.
+  __device__ __forceinline__ uint32_t top_finite() const {
+    constexpr uint32_t inf = DT == SPLICE_F32 ? 0x7F800000u : DT == SPLICE_BF16 ? 0x7F80u : 0x7C00u;
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      if (DT == SPLICE_F32) {
+        const uint32_t b = w[j] & 0x7FFFFFFFu;
+        m = max(m, b < inf ? b : 0u);
       } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
+        const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;
+        m = __vmaxu2(m, (lo < inf ? lo : 0u) | (hi < inf ? hi << 16 : 0u));
+      }
+    }
+    return m;
+  }
+  __device__ __forceinline__ void values(float* v) const {
+    if constexpr (DT == SPLICE_F32) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == SPLICE_BF16) {
+          v[2 * j] = __uint_as_float(w[j] << 16);
+          v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+          v[2 * j] = f.x;
+          v[2 * j + 1] = f.y;
+        }
       }
     }
   }
+};
+template <int DT>
+__device__ __forceinline__ uint32_t top_max(uint32_t a, uint32_t b) {
+  return DT == SPLICE_F32 ? max(a, b) : __vmaxu2(a, b);
 }
-
-// Largest finite magnitude of the eight values as its bit pattern (which
-// orders like the value), and whether any of them is not finite.
-__device__ __forceinline__ unsigned int amax8(const float* v, bool& special) {
-  unsigned int m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const unsigned int b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-    special |= b >= 0x7F800000u;
-    m = max(m, b >= 0x7F800000u ? 0u : b);
-  }
-  return m;
+// fp32 bits of the magnitude that top() describes; whether it is not finite.
+template <int DT>
+__device__ __forceinline__ uint32_t top_bits(uint32_t m) {
+  if constexpr (DT == SPLICE_F32) return m;
+  const uint32_t h = max(m & 0xFFFFu, m >> 16);
+  if constexpr (DT == SPLICE_BF16) return h << 16;
+  return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h))));
 }
+__device__ __forceinline__ bool bits_special(uint32_t b) { return b >= 0x7F800000u; }
 
 // Exponent s of the block's scale from the bits of its largest magnitude:
 // amax = f 2^e with f in [1, 2) and 448 = 1.75 * 2^8, so s = e - 8, or e - 7
@@ -71,7 +111,10 @@ __device__ __forceinline__ int scale_exp(unsigned int amax_bits) {
 
 // The eight codes of v * 2^-s.  Infinities become NaN codes (e4m3 has no
 // infinity, and the conversion would saturate them to a finite value).
-__device__ __forceinline__ uint2 codes8(const float* v, int s, bool special) {
+template <int DT>
+__device__ __forceinline__ uint2 codes8(const Raw8<DT>& r, int s, bool special) {
+  float v[8];
+  r.values(v);
   const float up = __uint_as_float(static_cast<unsigned int>(127 - s) << 23);  // s in [-127, 120]
   uint32_t h[4];
 #pragma unroll
@@ -99,7 +142,7 @@ __global__ void __launch_bounds__(QZ_THREADS) quantize_rows_kernel(const void* _
   pdl_trigger();
   const int l16 = threadIdx.x & 15;
   const unsigned int first = blockIdx.x * (QZ_THREADS / 16 * QZ_UNROLL) + (threadIdx.x >> 4);
-  float v[QZ_UNROLL][8];
+  Raw8<DT> v[QZ_UNROLL];
   unsigned int row[QZ_UNROLL];
   int kb[QZ_UNROLL];
 #pragma unroll
@@ -108,24 +151,29 @@ __global__ void __launch_bounds__(QZ_THREADS) quantize_rows_kernel(const void* _
     row[i] = u / static_cast<unsigned int>(KB);
     kb[i] = static_cast<int>(u - row[i] * KB);
     const int k = kb[i] * 128 + 8 * l16;
-    if (u < units && k < K) {
-      load8<DT>(x, row[i] * ldx + k, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    }
+    if (u < units && k < K)
+      v[i].load(x, row[i] * ldx + k);
+    else
+      v[i].clear();
   }
 #pragma unroll
   for (int i = 0; i < QZ_UNROLL; ++i) {
     const unsigned int u = first + i * (QZ_THREADS / 16);
-    bool special = false;
-    unsigned int m = amax8(v[i], special);
+    auto over_block = [](uint32_t m) {
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int o = 1; o < 16; o <<= 1) m = top_max<DT>(m, __shfl_xor_sync(0xffffffffu, m, o));
+      return top_bits<DT>(m);
+    };
+    uint32_t m = over_block(v[i].top());
+    const bool special = bits_special(m);
+    if (__any_sync(0xffffffffu, special)) {  // rare: the scale goes by the finite values
+      const uint32_t f = over_block(v[i].top_finite());
+      if (special) m = f;
+    }
     const int s = scale_exp(m);
     const int k = kb[i] * 128 + 8 * l16;
     if (u < units) {
-      if (k < K) *reinterpret_cast<uint2*>(codes + (long long)row[i] * K + k) = codes8(v[i], s, special);
+      if (k < K) *reinterpret_cast<uint2*>(codes + (long long)row[i] * K + k) = codes8<DT>(v[i], s, special);
       if (l16 == 0) scales[u] = static_cast<uint8_t>(s + 127);
     }
   }
@@ -145,30 +193,39 @@ __global__ void __launch_bounds__(QZ_THREADS) quantize_blocks_kernel(const void*
   const int mb = blockIdx.x / KB, kb = blockIdx.x - mb * KB;
   const int k = kb * 128 + 8 * (threadIdx.x & 15);
   const long long r0 = (long long)mb * 128 + (threadIdx.x >> 4);
-  float v[8][8];
+  Raw8<DT> v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (r0 + 16 * i < M && k < K) {
-      load8<DT>(x, (r0 + 16 * i) * ldx + k, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    }
+    if (r0 + 16 * i < M && k < K)
+      v[i].load(x, (r0 + 16 * i) * ldx + k);
+    else
+      v[i].clear();
   }
-  bool special = false;
-  unsigned int m = 0;
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, amax8(v[i], special));
-  m = __reduce_max_sync(0xffffffffu, m);
-  if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
-  __syncthreads();
+  for (int i = 0; i < 8; ++i) m = top_max<DT>(m, v[i].top());
+  auto over_block = [&](uint32_t bits) {
+    bits = __reduce_max_sync(0xffffffffu, bits);
+    if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = bits;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < QZ_THREADS / 32; ++i) m = max(m, wmax[i]);
-  const int s = scale_exp(m);
+    for (int i = 0; i < QZ_THREADS / 32; ++i) bits = max(bits, wmax[i]);
+    return bits;
+  };
+  uint32_t top = over_block(top_bits<DT>(m));
+  const bool special = bits_special(top);
+  if (special) {  // rare, the whole block together: the scale goes by the finite values
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = top_max<DT>(m, v[i].top_finite());
+    __syncthreads();  // wmax has been read
+    top = over_block(top_bits<DT>(m));
+  }
+  const int s = scale_exp(top);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (r0 + 16 * i < M && k < K)
-      *reinterpret_cast<uint2*>(codes + (r0 + 16 * i) * K + k) = codes8(v[i], s, special);
+      *reinterpret_cast<uint2*>(codes + (r0 + 16 * i) * K + k) = codes8<DT>(v[i], s, special);
   if (threadIdx.x == 0) scales[blockIdx.x] = static_cast<uint8_t>(s + 127);
 }
 
@@ -214,10 +271,15 @@ struct Fp8Params {
   int KB;
 };
 
-template <int BN_>
+template <int EPI>
+constexpr bool epi_wide() {  // 16-bit outputs stored as they are: 64 columns = 128-byte rows
+  return (EPI & ~EPI_GELU) == 0;
+}
+
+template <int BN_, bool WIDE>
 struct Fp8Shape {
   static constexpr int BM = 128, BN = BN_, BK = 128;
-  static constexpr int STAGES = BN >= 128 ? 6 : 8;
+  static constexpr int STAGES = BN == 192 ? 4 : BN == 128 ? 5 : 8;
   static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int ACC_COLS = BN;
   static constexpr int SF_A = 4, SF_B = BN / 32, SF_COLS = (SF_A + SF_B + 3) / 4 * 4;  // columns of one scale slot
@@ -225,12 +287,15 @@ struct Fp8Shape {
   static constexpr int SF_BASE = 2 * ACC_COLS;
   static constexpr int TMEM_USED = SF_BASE + SF_SLOTS * SF_COLS;
   static constexpr int TMEM_COLS = TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
-  static constexpr int EPI_WARPS = 8, SF_WARPS = 4;
+  // epilogue warps: four per 64 columns (wide), or two column parts of 32-column groups
+  static constexpr int PARTS = !WIDE ? 2 : (BN + 63) / 64, EPI_WARPS = 4 * PARTS, SF_WARPS = 4;
   static constexpr int THREADS = 32 * (2 + EPI_WARPS + SF_WARPS);
-  static constexpr int EPI_BUF_BYTES = EPI_WARPS * 4096;
+  static constexpr int NBUF = 1, EPI_BUF_BYTES = EPI_WARPS * 4096 * NBUF;
   static constexpr int BARS = 2 * STAGES + 4 + 2 * SF_SLOTS + 1;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BUF_BYTES + 8 * BARS + 16;
-  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+  static constexpr int BIAS_BYTES = WIDE ? EPI_WARPS * 256 : 0;
+  static constexpr int SF_DEPTH = 8, SF_ROWS = 128 + 8, SF_BYTES = SF_DEPTH * SF_ROWS * 8;  // scale bytes on their way
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BUF_BYTES + BIAS_BYTES + SF_BYTES + 8 * BARS + 16;
+  static_assert(SMEM_BYTES <= 227 * 1024 - 16, "shared memory");
   static_assert(TMEM_USED <= 512, "tensor memory");
 };
 
@@ -242,28 +307,114 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N) {
 __device__ __forceinline__ uint32_t idesc_sf(uint32_t idesc, int byte) {
   return idesc | (static_cast<uint32_t>(byte) << 4) | (static_cast<uint32_t>(byte) << 29);
 }
-__device__ __forceinline__ void tc_mma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+// The four K = 32 steps of a 128-element k-block.  Written for a whole warp in
+// step, one elected lane issuing: the operands then stay in uniform registers
+// (a lone lane's are moved there for every instruction; 6240 x 1280 x 5120
+// took 86 us that way, 40 this way).
+__device__ __forceinline__ void tc_mma4_mxf8(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
-          d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %7, %8, %3, [%5], [%6], 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %9, %10, %3, [%5], [%6], 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %11, %12, %3, [%5], [%6], 1;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "l"(ad + 2), "l"(bd + 2), "l"(ad + 4),
+        "l"(bd + 4), "l"(ad + 6), "l"(bd + 6)
+        : "memory");
+}
+// Commit of the elected lane's MMAs.
+__device__ __forceinline__ void tc_commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// Barrier of the four scale warps.
+__device__ __forceinline__ void sf_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // One 32-bit column of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
 }
 
-// The four scale bytes of k-blocks 4 g .. 4 g + 3 of one row (1.0 past the end).
-__device__ __forceinline__ uint32_t sf_word(const uint8_t* row, int g, int KB, bool valid, bool word_ok) {
-  if (!valid) return 0x7F7F7F7Fu;
-  if (word_ok) return __ldg(reinterpret_cast<const unsigned int*>(row + 4 * g));
-  uint32_t w = 0;
+// Starts the copy of the scale bytes of k-blocks 4 g .. 4 g + 3 of row r of
+// scales [rows, KB] to dst: the aligned words around them (a row of whole
+// words fills only the first), from which sf_bytes picks them.  Where a word
+// would reach past the array, or the array is not aligned, bytes are read one
+// by one.  What follows the row's last byte is never used.
+__device__ __forceinline__ void sf_copy(uint2* dst, const uint8_t* sc, long long r, long long rows, int g, int KB, bool aligned) {
+  const long long off = r * KB + 4 * g;
+  const int sh = static_cast<int>(off & 3);
+  if (aligned && off - sh + (sh ? 8 : 4) <= rows * KB) {
+    cp_async_4(&dst->x, sc + (off - sh));
+    if (sh) cp_async_4(&dst->y, sc + (off - sh) + 4);
+  } else {
+    uint64_t v = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w |= (4 * g + j < KB ? static_cast<uint32_t>(__ldg(row + 4 * g + j)) : 0x7Fu) << (8 * j);
-  return w;
+    for (int j = 0; j < 4; ++j)
+      if (4 * g + j < KB) v |= static_cast<uint64_t>(__ldg(sc + off + j)) << (8 * (sh + j));
+    *dst = make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
+  }
+}
+__device__ __forceinline__ uint32_t sf_bytes(uint2 v, long long r, int KB) {
+  return __funnelshift_r(v.x, v.y, 8 * (static_cast<int>(r) * KB & 3));
+}
+
+// Epilogue of one warp for 16-bit outputs: its 32 rows and COLS (64, or
+// a 32-wide tile's 32) columns are read
+// into registers at once (the accumulator goes back to the MMAs before any of
+// the arithmetic), get bias and GELU, and leave as one TMA store of 128-byte
+// rows.  (48000 x 18432 x 768 on 128 x 128 tiles: 1141 us through the engine's
+// epilogue, whose boxes are 32 columns and which holds the accumulator
+// throughout; 842 us this way, with the scales loaded as below.)
+template <int COLS, int EPI, int KIND, typename Release>
+__device__ __forceinline__ void epilogue_wide(const GemmParams& p, const CUtensorMap* tm_out, uint32_t taddr, int row0,
+                                              int n, int lane, uint8_t* buf, bool other_buf, const float* bias,
+                                              Release release) {
+  float v[COLS];
+#pragma unroll
+  for (int c = 0; c < COLS; c += 32) tmem_ld32(taddr + c, v + c);
+  tmem_ld_wait();
+  tc_fence_before();
+  __syncwarp();
+  release();
+  if (row0 >= p.M || n >= p.N) return;  // the whole warp
+  if (p.bias) {
+#pragma unroll
+    for (int k = 0; k < COLS / 4; ++k) {
+      const float4 b = reinterpret_cast<const float4*>(bias)[k];  // the same address in every lane
+      v[4 * k] += b.x, v[4 * k + 1] += b.y, v[4 * k + 2] += b.z, v[4 * k + 3] += b.w;
+    }
+  }
+  if constexpr ((EPI & EPI_GELU) != 0) {
+#pragma unroll
+    for (int k = 0; k < COLS; k += 2) {
+      const float2 g = gelu_erf2(make_float2(v[k], v[k + 1]));
+      v[k] = g.x, v[k + 1] = g.y;
+    }
+  }
+  // the store that last used this buffer has read it
+  if (lane == 0) {
+    if (other_buf)
+      bulk_wait_read1();
+    else
+      bulk_wait_read0();
+  }
+  __syncwarp();
+  // the 128-byte (or, for 32 columns, 64-byte) swizzle of the store
+  uint4* row = reinterpret_cast<uint4*>(buf + lane * (2 * COLS));
+  const int x = COLS == 64 ? lane & 7 : (lane >> 1) & 3;
+#pragma unroll
+  for (int k = 0; k < COLS / 8; ++k) row[k ^ x] = pack8_16<KIND>(v + 8 * k);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(tm_out, buf, n, row0);
+    bulk_commit();
+  }
 }
 
 }  // namespace
@@ -273,10 +424,10 @@ __device__ __forceinline__ uint32_t sf_word(const uint8_t* row, int g, int KB, b
 // the scale ring filled.  Waits are bounded; a role that gives up marks the
 // CTA in shared memory, and the CTA reports it to p.status at its end.
 template <int BN, int EPI, int KIND>
-__global__ void __launch_bounds__(Fp8Shape<BN>::THREADS, 1)
+__global__ void __launch_bounds__(Fp8Shape<BN, epi_wide<EPI>()>::THREADS, 1)
     gemm_fp8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmOut, const GemmParams p, const Fp8Params f) {
-  using S = Fp8Shape<BN>;
+  using S = Fp8Shape<BN, epi_wide<EPI>()>;
   constexpr int STAGES = S::STAGES;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int failed;
@@ -284,7 +435,9 @@ __global__ void __launch_bounds__(Fp8Shape<BN>::THREADS, 1)
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES * S::A_BYTES;
   uint8_t* sEpi = smem + STAGES * S::STAGE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + S::EPI_BUF_BYTES);
+  float* sBias = reinterpret_cast<float*>(sEpi + S::EPI_BUF_BYTES);
+  uint2* sSf = reinterpret_cast<uint2*>(sEpi + S::EPI_BUF_BYTES + S::BIAS_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + S::EPI_BUF_BYTES + S::BIAS_BYTES + S::SF_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
@@ -292,7 +445,7 @@ __global__ void __launch_bounds__(Fp8Shape<BN>::THREADS, 1)
   uint64_t* sempty = sfull + S::SF_SLOTS;
   uint64_t* drain = sempty + S::SF_SLOTS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     failed = 0;
@@ -334,101 +487,155 @@ __global__ void __launch_bounds__(Fp8Shape<BN>::THREADS, 1)
       }
       // every issued load lands before the CTA exits
       for (int s = 0; s < STAGES && s < it; ++s)
-        mbar_wait_bounded(&full[s], ((it - 1 - s) / STAGES) & 1, kDrainLimitNs, nullptr, 0);
+        mbar_wait(&full[s], ((it - 1 - s) / STAGES) & 1, kDrainLimitNs, nullptr, 0);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_mxf8(S::BM, BN);
-      int it = 0, tl = 0, sg = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < p.num_tiles && ok; t += gridDim.x, ++tl) {
-        const int a = tl & 1;
-        if (!(ok = mbar_wait(&tempty[a], ((tl >> 1) & 1) ^ 1, p.limit_ns, &failed, DEV_TIMEOUT_MMA))) break;
-        const uint32_t d = tmem + a * S::ACC_COLS;
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
-          const int s = it % STAGES, slot = sg % S::SF_SLOTS;
-          if ((kb & 3) == 0 && !(ok = mbar_wait(&sfull[slot], (sg / S::SF_SLOTS) & 1, p.limit_ns, &failed,
-                                                        DEV_TIMEOUT_MMA)))
-            break;
-          if (!(ok = mbar_wait(&full[s], (it / STAGES) & 1, p.limit_ns, &failed, DEV_TIMEOUT_MMA))) break;
-          tc_fence_after();
-          const uint64_t ad = sw128_kmajor_desc(smem_u32(sA + s * S::A_BYTES));
-          const uint64_t bd = sw128_kmajor_desc(smem_u32(sB + s * S::B_BYTES));
-          const uint32_t sf = tmem + S::SF_BASE + slot * S::SF_COLS;
-          const uint32_t id = idesc_sf(idesc, kb & 3);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_mxf8(d, ad + 2 * k, bd + 2 * k, id, sf, sf + S::SF_A, (kb > 0 || k > 0) ? 1u : 0u);
-          tc_commit(&empty[s]);
-          if ((kb & 3) == 3 || kb == p.k_blocks - 1) {
-            tc_commit(&sempty[slot]);
-            ++sg;
-          }
+    constexpr uint32_t idesc = idesc_mxf8(S::BM, BN);
+    const uint64_t ad0 = sw128_kmajor_desc(smem_u32(sA)), bd0 = sw128_kmajor_desc(smem_u32(sB));
+    auto wait = [&](uint64_t* b, int n) {
+      return __all_sync(0xffffffffu, mbar_wait(b, n & 1, p.limit_ns, &failed, DEV_TIMEOUT_MMA)) != 0;
+    };
+    int it = 0, tl = 0, sg = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < p.num_tiles && ok; t += gridDim.x, ++tl) {
+      const int a = tl & 1;
+      if (!(ok = wait(&tempty[a], (tl >> 1) ^ 1))) break;
+      const uint32_t d = tmem + a * S::ACC_COLS;
+      for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+        const int s = it % STAGES, slot = sg % S::SF_SLOTS;
+        if ((kb & 3) == 0 && !(ok = wait(&sfull[slot], sg / S::SF_SLOTS))) break;
+        if (!(ok = wait(&full[s], it / STAGES))) break;
+        tc_fence_after();
+        const uint32_t sf = tmem + S::SF_BASE + slot * S::SF_COLS;
+        tc_mma4_mxf8(d, ad0 + s * (S::A_BYTES >> 4), bd0 + s * (S::B_BYTES >> 4), idesc_sf(idesc, kb & 3), sf,
+                            sf + S::SF_A, kb > 0 ? 1u : 0u);
+        tc_commit_elect(&empty[s]);
+        if ((kb & 3) == 3 || kb == p.k_blocks - 1) {
+          tc_commit_elect(&sempty[slot]);
+          ++sg;
         }
-        if (!ok) break;
-        tc_commit(&tfull[a]);
       }
-      // all issued MMAs complete before tensor memory is released
-      tc_commit(drain);
-      mbar_wait_bounded(drain, 0, kDrainLimitNs, nullptr, 0);
+      if (!ok) break;
+      tc_commit_elect(&tfull[a]);
     }
+    // all issued MMAs complete before tensor memory is released
+    tc_commit_elect(drain);
+    mbar_wait(drain, 0, kDrainLimitNs, nullptr, 0);
   } else if (warp < 2 + S::EPI_WARPS) {
-    const int q = warp & 3, half = (warp - 2) / 4;
+    const int q = warp & 3, part = (warp - 2) / 4;
     int tl = 0, gcount = 0;
     for (int t = blockIdx.x; t < p.num_tiles; t += gridDim.x, ++tl) {
       const int a = tl & 1;
       int mb, nb;
       tile_coords(p, t, mb, nb);
-      float breg[4];
-      load_bias(p, nb * BN, BN, half, lane, breg);
-      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[a], (tl >> 1) & 1, p.limit_ns, &failed, DEV_TIMEOUT_EPILOGUE)))
-        break;
-      tc_fence_after();
       const int m0 = mb * S::BM;
-      epilogue_warp<EPI, KIND>(p, &tmOut, tmem + (static_cast<uint32_t>(32 * q) << 16) + a * S::ACC_COLS, m0 + 32 * q,
-                               min(m0 + 128, p.M), nb * BN, BN, half, lane, sEpi + (warp - 2) * 4096, breg, PIECE_FULL,
-                               64, &gcount);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[a]);
+      const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16) + a * S::ACC_COLS;
+      uint8_t* buf = sEpi + (warp - 2) * 4096 * S::NBUF;
+      auto wait = [&] {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[a], (tl >> 1) & 1, p.limit_ns, &failed, DEV_TIMEOUT_EPILOGUE));
+        tc_fence_after();
+        return ok;
+      };
+      auto release = [&] {
+        if (lane == 0) mbar_arrive(&tempty[a]);
+      };
+      if constexpr (epi_wide<EPI>()) {
+        // the columns' biases, fetched while the accumulator is not ready
+        constexpr int COLS = BN < 64 ? BN : 64;
+        float* bias = sBias + (warp - 2) * 64;
+        const int n = nb * BN + 64 * part;
+        __syncwarp();  // the last tile's biases have been read
+        if (p.bias) {
+          for (int c = lane; c < COLS; c += 32) bias[c] = n + c < p.N ? __ldg(p.bias + n + c) : 0.f;
+        }
+        __syncwarp();
+        if (!wait()) break;
+        epilogue_wide<COLS, EPI, KIND>(p, &tmOut, acc + 64 * part, m0 + 32 * q, n, lane,
+                                       buf + (S::NBUF == 2 ? (tl & 1) * 4096 : 0), S::NBUF == 2, bias, release);
+      } else {
+        if (EPI & EPI_RESID) epilogue_prefetch_l2(p, t, part, q, lane, BN, S::BM, 0);
+        float breg[4];
+        load_bias(p, nb * BN, BN, part, lane, breg);
+        if (!wait()) break;
+        epilogue_warp<EPI, KIND>(p, &tmOut, acc, m0 + 32 * q, min(m0 + 128, p.M), nb * BN, BN, part, lane, buf, breg,
+                                 PIECE_FULL, 64, &gcount);
+        tc_fence_before();
+        __syncwarp();
+        release();
+      }
     }
     if (lane == 0) bulk_wait0();
   } else {
+    // Scales.  The four warps share out the bytes of a slot (32 rows of A each,
+    // the first also B's) as asynchronous copies, SF_DEPTH slots ahead, and
+    // each writes all of them to its own lane quarter.  The depth is what
+    // matters: beside the output's writes a load takes over 2000 clocks, and
+    // loading one or two slots ahead left the MMAs waiting 2600 clocks a tile.
     const int q = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-    // whole words where every row of scales starts on a 4-byte boundary
-    const bool word_ok = f.KB % 4 == 0 && ((reinterpret_cast<uintptr_t>(f.xs) | reinterpret_cast<uintptr_t>(f.ws)) & 3) == 0;
-    int sg = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < p.num_tiles && ok; t += gridDim.x) {
-      int mb, nb;
-      tile_coords(p, t, mb, nb);
-      for (int g = 0; g < groups; ++g, ++sg) {
-        const int slot = sg % S::SF_SLOTS;
-        uint32_t w[S::SF_A + S::SF_B];
-#pragma unroll
-        for (int c = 0; c < S::SF_A; ++c) {
-          const int m = mb * S::BM + 32 * c + lane;
-          w[c] = sf_word(f.xs + (long long)m * f.KB, g, f.KB, m < p.M, word_ok);
-        }
-#pragma unroll
-        for (int c = 0; c < S::SF_B; ++c) {
-          const int n = nb * BN + 32 * c + lane;
-          w[S::SF_A + c] = sf_word(f.ws + (long long)(n >> 7) * f.KB, g, f.KB, n < p.N, word_ok);
-        }
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sempty[slot], ((sg / S::SF_SLOTS) & 1) ^ 1, p.limit_ns,
-                                                             &failed, DEV_TIMEOUT_GATHER))))
-          break;
-        tc_fence_after();
-        const uint32_t dst = tmem + S::SF_BASE + slot * S::SF_COLS + lanes;
-#pragma unroll
-        for (int c = 0; c < S::SF_A + S::SF_B; ++c) tmem_st1(dst + c, w[c]);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull[slot]);
+    const bool xs_al = (reinterpret_cast<uintptr_t>(f.xs) & 3) == 0, ws_al = (reinterpret_cast<uintptr_t>(f.ws) & 3) == 0;
+    const int items = p.num_tiles > (int)blockIdx.x ? ((p.num_tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * groups : 0;
+    struct Item {  // the k-th (tile, slot) of this block
+      int t, g, mb, nb;
+    };
+    auto advance = [&](Item& i) {
+      if (++i.g == groups) {
+        i.g = 0;
+        i.t += gridDim.x;
+        tile_coords(p, i.t, i.mb, i.nb);
       }
+    };
+    Item ahead = {static_cast<int>(blockIdx.x), 0, 0, 0};
+    tile_coords(p, ahead.t, ahead.mb, ahead.nb);
+    Item cur = ahead;
+    int n_ahead = 0;
+    auto copy = [&] {  // one group per call, empty past the end
+      if (n_ahead < items) {
+        uint2* dst = sSf + n_ahead % S::SF_DEPTH * S::SF_ROWS;
+        const int m = ahead.mb * S::BM + 32 * q + lane, n = ahead.nb * BN + 32 * lane;
+        if (m < p.M) sf_copy(dst + 32 * q + lane, f.xs, m, p.M, ahead.g, f.KB, xs_al);
+        // a column's 32 rows of B share one 128-row block
+        if (q == 0 && lane < S::SF_B && n < p.N) sf_copy(dst + 128 + lane, f.ws, n >> 7, (p.N + 127) / 128, ahead.g, f.KB, ws_al);
+        advance(ahead);
+        ++n_ahead;
+      }
+      cp_async_commit();
+    };
+    for (int i = 0; i < S::SF_DEPTH - 1; ++i) copy();
+    // After a failed wait the loop runs on without waiting: the four warps
+    // meet the same barriers.
+    bool ok = true;
+    for (int i = 0; i < items; ++i) {
+      cp_async_wait<S::SF_DEPTH - 2>();
+      sf_sync();  // slot i has arrived, slot i - 1 has been read by all
+      copy();
+      const uint2* src = sSf + i % S::SF_DEPTH * S::SF_ROWS;
+      uint32_t w[S::SF_A + S::SF_B];
+#pragma unroll
+      for (int c = 0; c < S::SF_A; ++c) {
+        const int m = cur.mb * S::BM + 32 * c + lane;
+        // rows past the end: any finite scale
+        w[c] = m < p.M ? sf_bytes(src[32 * c + lane], m, f.KB) : 0x7F7F7F7Fu;
+      }
+#pragma unroll
+      for (int c = 0; c < S::SF_B; ++c) {
+        const int n = cur.nb * BN + 32 * c;
+        w[S::SF_A + c] = n < p.N ? sf_bytes(src[128 + c], n >> 7, f.KB) : 0x7F7F7F7Fu;
+      }
+      advance(cur);
+      const int slot = i % S::SF_SLOTS;
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&sempty[slot], ((i / S::SF_SLOTS) & 1) ^ 1, p.limit_ns, &failed,
+                                                   DEV_TIMEOUT_GATHER));
+      tc_fence_after();
+      const uint32_t dst = tmem + S::SF_BASE + slot * S::SF_COLS + lanes;
+#pragma unroll
+      for (int c = 0; c < S::SF_A + S::SF_B; ++c) tmem_st1(dst + c, w[c]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(&sfull[slot]);
     }
+    cp_async_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -442,7 +649,7 @@ namespace {
 template <int BN, int EPI, int KIND = KIND_BF16>
 cudaError_t run_fp8(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const GemmParams& p,
                     const Fp8Params& f, int grid, cudaStream_t st) {
-  using S = Fp8Shape<BN>;
+  using S = Fp8Shape<BN, epi_wide<EPI>()>;
   auto k = gemm_fp8_tc_kernel<BN, EPI, KIND>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES);
   if (e != cudaSuccess) return e;
@@ -453,7 +660,8 @@ template <int BN>
 cudaError_t run_fp8_epi(int epi, bool f16, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
                         const GemmParams& p, const Fp8Params& f, int grid, cudaStream_t st) {
   switch (epi) {
-    case 0: return f16 ? run_fp8<BN, 0, KIND_F16>(a, b, o, p, f, grid, st) : run_fp8<BN, 0>(a, b, o, p, f, grid, st);
+    case 0:
+      return f16 ? run_fp8<BN, 0, KIND_F16>(a, b, o, p, f, grid, st) : run_fp8<BN, 0>(a, b, o, p, f, grid, st);
     case EPI_GELU: return run_fp8<BN, EPI_GELU>(a, b, o, p, f, grid, st);
     case EPI_OUT_F32: return run_fp8<BN, EPI_OUT_F32>(a, b, o, p, f, grid, st);
     case EPI_RESID: return run_fp8<BN, EPI_RESID>(a, b, o, p, f, grid, st);
@@ -466,20 +674,41 @@ cudaError_t run_fp8_epi(int epi, bool f16, const CUtensorMap& a, const CUtensorM
 
 cudaError_t launch_linear_fp8(const void* x, const uint8_t* xs, const void* w, const uint8_t* ws, GemmParams p, int epi,
                               bool f16, int num_sms, cudaStream_t st) {
-  const bool narrow = (p.M + 127) / 128 * ((p.N + 127) / 128) * 2 <= num_sms;
-  const int bn = narrow ? 32 : 128;
+  // The tile width with the least waves x time of a tile.  A k-block of a
+  // 128 x 32, 128 or 192 tile takes 0.20, 0.25 or 0.29 us alone on its SM
+  // (64 x 1280 x 5120: 10.4, 12.3 and 14.2 us); wider ones move fewer bytes per
+  // product and win once every SM has work (6240 x 1280 x 5120: 128 40.9, 192
+  // 38.0 us; 5 x 768 x 768: 32 4.1, 128 4.5 us; 780 x 1280 x 1280: 128 6.0,
+  // 192 7.1 us).  CTA pairs (256 x 192) were slower throughout: 53.7 us at
+  // 6240 x 1280 x 5120.
+  const int mb = (p.M + 127) / 128;
+  int bn = 0;
+  long long least = 0;
+  for (const auto& c : {std::pair<int, int>{32, 20}, {128, 25}, {192, 29}}) {
+    const long long waves = ((long long)mb * ((p.N + c.first - 1) / c.first) + num_sms - 1) / num_sms;
+    if (!bn || waves * c.second < least) bn = c.first, least = waves * c.second;
+  }
   CUtensorMap a, b, o;
   if (!make_tmap_u8(&a, x, p.M, p.K, 128) || !make_tmap_u8(&b, w, p.N, p.K, bn)) return cudaErrorInvalidValue;
-  p.out_tma = !(epi & EPI_SWIGLU) && make_tmap_out(&o, p.out, p.M, p.N, p.ldo, (epi & (EPI_OUT_F32 | EPI_RESID)) != 0);
-  if (!p.out_tma) o = b;
-  p.m_blocks = (p.M + 127) / 128;
+  if ((epi & ~EPI_GELU) == 0) {
+    if (!(bn == 32 ? make_tmap_out(&o, p.out, p.M, p.N, p.ldo, false) : make_tmap_bf16(&o, p.out, p.M, p.N, p.ldo, 32)))
+      return cudaErrorInvalidValue;
+  } else {
+    p.out_tma = !(epi & EPI_SWIGLU) && make_tmap_out(&o, p.out, p.M, p.N, p.ldo, true);
+    if (!p.out_tma) o = b;
+  }
+  p.m_blocks = mb;
   p.n_blocks = (p.N + bn - 1) / bn;
   p.k_blocks = (p.K + 127) / 128;
   p.num_tiles = p.m_blocks * p.n_blocks;
   p.n_fast = p.M > p.N;
   const Fp8Params f = {xs, ws, p.k_blocks};
   const int grid = std::min(p.num_tiles, num_sms);
-  return narrow ? run_fp8_epi<32>(epi, f16, a, b, o, p, f, grid, st) : run_fp8_epi<128>(epi, f16, a, b, o, p, f, grid, st);
+  switch (bn) {
+    case 32: return run_fp8_epi<32>(epi, f16, a, b, o, p, f, grid, st);
+    case 128: return run_fp8_epi<128>(epi, f16, a, b, o, p, f, grid, st);
+    default: return run_fp8_epi<192>(epi, f16, a, b, o, p, f, grid, st);
+  }
 }
 
 }  // namespace asr

@@ -398,8 +398,8 @@ cudaError_t launch_xattn(XattnArgs a, int n_seg, int max_k, bool f16, int num_sm
   const int tiles = (int)(((long long)a.max_q * a.G + 15) / 16), Hkv = a.H / a.G;
   a.splits = pick_splits((long long)n_seg * tiles * Hkv, max_k, XS_WARPS * XS_KEYS, 2LL * num_sms);
   const dim3 grid(n_seg * a.splits, tiles, Hkv);
-  return f16 ? launch_split(xattn_rows_kernel<KIND_F16>, grid, 32 * XS_WARPS, 0, a.splits, st, a)
-             : launch_split(xattn_rows_kernel<KIND_BF16>, grid, 32 * XS_WARPS, 0, a.splits, st, a);
+  return f16 ? launch_cluster(xattn_rows_kernel<KIND_F16>, grid, 32 * XS_WARPS, 0, a.splits, st, a)
+             : launch_cluster(xattn_rows_kernel<KIND_BF16>, grid, 32 * XS_WARPS, 0, a.splits, st, a);
 }
 
 cudaError_t launch_xattn_weights(XattnArgs a, int n_seg, int n_sel, bool f16, int num_sms, cudaStream_t st) {
@@ -408,10 +408,10 @@ cudaError_t launch_xattn_weights(XattnArgs a, int n_seg, int n_sel, bool f16, in
   a.splits = pick_splits((long long)n_seg * tiles * n_sel, a.width, XW_WARPS * XW_KEYS, num_sms);
   const dim3 grid(n_seg * a.splits, tiles, n_sel);
   if (wide)
-    return f16 ? launch_split(xattn_weights_kernel<KIND_F16, 4>, grid, 32 * XW_WARPS, 0, a.splits, st, a)
-               : launch_split(xattn_weights_kernel<KIND_BF16, 4>, grid, 32 * XW_WARPS, 0, a.splits, st, a);
-  return f16 ? launch_split(xattn_weights_kernel<KIND_F16, 1>, grid, 32 * XW_WARPS, 0, a.splits, st, a)
-             : launch_split(xattn_weights_kernel<KIND_BF16, 1>, grid, 32 * XW_WARPS, 0, a.splits, st, a);
+    return f16 ? launch_cluster(xattn_weights_kernel<KIND_F16, 4>, grid, 32 * XW_WARPS, 0, a.splits, st, a)
+               : launch_cluster(xattn_weights_kernel<KIND_BF16, 4>, grid, 32 * XW_WARPS, 0, a.splits, st, a);
+  return f16 ? launch_cluster(xattn_weights_kernel<KIND_F16, 1>, grid, 32 * XW_WARPS, 0, a.splits, st, a)
+             : launch_cluster(xattn_weights_kernel<KIND_BF16, 1>, grid, 32 * XW_WARPS, 0, a.splits, st, a);
 }
 
 }  // namespace asr

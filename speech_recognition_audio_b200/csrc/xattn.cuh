@@ -47,24 +47,6 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 // exp(-inf - m) is 0 there and not NaN.
 __device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.f : m; }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_split(void (*k)(KArgs...), dim3 grid, int threads, size_t smem, int splits, cudaStream_t st, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = splits;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k, std::forward<Args>(args)...);
-}
-
 // Blocks a (segment, tile, head) is split into: a power of two up to the
 // portable cluster size, while the grid does not yet fill `fill` blocks and
 // each block keeps at least `least` keys.
