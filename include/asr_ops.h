@@ -237,8 +237,9 @@ asr_status asr_op_cross_attention_check(const void* ws, void* stream);
  *                      (q[i, heads[s]] . k[n, heads[s] / G] / 8)
  * in fp32, n counted from the segment's first state.  Columns n from the
  * segment's states to max_k are zero; rows outside every segment are left.
- *  heads    device int32 [n_sel], the query heads wanted (a value outside
- *           [0, H) sets the status word to 7 and writes nothing).
+ *  heads    device int32 [n_sel], the query heads wanted, n_sel <= 65535 (a
+ *           value outside [0, H) sets the status word to 7 and writes
+ *           nothing), or NULL with n_sel == H: all heads in order.
  *  weights  device float32 [n_sel, Tq, ldw], ldw >= max_k (rows of whole 32
  *           bytes, ldw % 8 == 0 and an aligned pointer, are written fastest);
  *           columns from max_k to ldw are not touched.

@@ -469,47 +469,66 @@ def gelu(x, stream=None):
     return y
 
 
+_torch = None
+
+
+def _t():
+    """torch, imported at the first call (the geometry queries need none)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _operands(what, *tensors):
-    """Refuse operands that are not on the current device."""
-    import torch
-    dev = torch.cuda.current_device()
+    """Refuse operands that are not on the current device; returns its index."""
+    dev = _t().cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"{what}: every tensor must be on the current CUDA device")
+    return dev
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)  # current_stream() without the Python object
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _rows(what, t, cols=None):
-    """Refuse anything but a 2-D tensor of contiguous elements within each row."""
+    """Refuse anything but a 2-D tensor of contiguous elements within each row; returns its row stride."""
     if t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1 or (cols is not None and t.shape[1] != cols):
         raise ValueError(f"{what}: need a 2-D tensor with contiguous rows" + (f" of {cols}" if cols is not None else ""))
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
-def _allocating(stream):
-    """Context in which torch allocates for `stream`, so that what a call allocates and drops is not
-    handed out again before that stream is done with it."""
-    import contextlib
-    import torch
+def _new(stream, shape, dtype, like, zero=False):
+    """A tensor allocated for `stream`, so that what a call allocates and drops is not handed out again
+    before that stream is done with it."""
+    torch = _torch
+    make = torch.zeros if zero else torch.empty
     if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        return make(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        return make(shape, dtype=dtype, device=like.device)
 
 
 def quantize_fp8(x, block_rows: int = 1, stream=None):
     """x CUDA [M, K] (bf16 / f16 / f32, rows may be strided) -> (codes float8_e4m3fn [M, K], scales
     float8_e8m0fnu [ceil(M / block_rows), ceil(K / 128)]), one power-of-two scale per block of block_rows
     (1 or 128) x 128 (asr_op_quantize_fp8)."""
-    import torch
-    _operands("quantize_fp8", x)
-    _rows("quantize_fp8", x)
-    code = _DTYPE_CODE.get(str(x.dtype)[6:])
+    torch = _t()
+    dev = _operands("quantize_fp8", x)
+    ldx = _rows("quantize_fp8", x)
+    code = 0 if x.dtype is torch.bfloat16 else 1 if x.dtype is torch.float32 else 2 if x.dtype is torch.float16 else None
     if code is None:
         raise ValueError(f"quantize_fp8: {x.dtype} is not bf16, f16 or f32")
     M, K = x.shape
-    with _allocating(stream):
-        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
-        scales = torch.empty((-(-M // max(block_rows, 1)), -(-K // 128)), dtype=torch.float8_e8m0fnu, device=x.device)
-    _check(lib.asr_op_quantize_fp8(x.data_ptr(), code, x.stride(0), M, K, block_rows, codes.data_ptr(),
-                                   scales.data_ptr(), _stream(stream)))
+    codes = _new(stream, (M, K), torch.float8_e4m3fn, x)
+    scales = _new(stream, (-(-M // max(block_rows, 1)), -(-K // 128)), torch.float8_e8m0fnu, x)
+    _check(lib.asr_op_quantize_fp8(x.data_ptr(), code, ldx, M, K, block_rows, codes.data_ptr(), scales.data_ptr(),
+                                   _raw_stream(stream, dev)))
     return codes, scales
 
 
@@ -518,58 +537,59 @@ def linear_fp8(x, x_scales, w, w_scales, bias=None, epi: int = EPI_BF16, out=Non
     quantize_fp8(w, 128)), bias f32 [N] -> epilogue(x w^T + bias) (asr_op_linear_fp8).  workspace: a zeroed
     CUDA tensor of asr_op_linear_fp8_ws_size() bytes whose first int32 the call sets if a device wait gives up;
     a program that calls this often keeps one."""
-    import torch
-    _operands("linear_fp8", x, x_scales, w, w_scales, bias, out, workspace)
+    torch = _t()
+    dev = _operands("linear_fp8", x, x_scales, w, w_scales, bias, out, workspace)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("linear_fp8: x and w must be 2-D")
     M, K = x.shape
     N = w.shape[0]
     KB = -(-K // 128)
-    if not (x.dtype == w.dtype == torch.float8_e4m3fn and x_scales.dtype == w_scales.dtype == torch.float8_e8m0fnu):
+    e4m3, e8m0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    if x.dtype is not e4m3 or w.dtype is not e4m3 or x_scales.dtype is not e8m0 or w_scales.dtype is not e8m0:
         raise ValueError("linear_fp8: codes must be float8_e4m3fn and scales float8_e8m0fnu")
-    if (w.shape[1] != K or tuple(x_scales.shape) != (M, KB) or tuple(w_scales.shape) != (-(-N // 128), KB) or not (
+    if (w.shape[1] != K or x_scales.shape != (M, KB) or w_scales.shape != (-(-N // 128), KB) or not (
             x.is_contiguous() and w.is_contiguous() and x_scales.is_contiguous() and w_scales.is_contiguous())):
         raise ValueError("linear_fp8: need contiguous x [M, K], w [N, K], x_scales [M, ceil(K/128)] and "
                          "w_scales [ceil(N/128), ceil(K/128)]")
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,) or not bias.is_contiguous()):
+    if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (N,) or not bias.is_contiguous()):
         raise ValueError("linear_fp8: bias must be contiguous float32 [N]")
     dt = torch.float32 if epi in (EPI_F32, EPI_F32_RESID) else torch.float16 if epi == EPI_F16 else torch.bfloat16
     shape = (M, N // 2 if epi == EPI_SWIGLU else N)
-    with _allocating(stream):
-        if out is None:
-            if epi == EPI_F32_RESID:
-                raise ValueError("EPI_F32_RESID needs `out` (updated in place)")
-            out = torch.empty(shape, dtype=dt, device=x.device)
-        elif out.dtype != dt or tuple(out.shape) != shape or not out.is_contiguous():
-            raise ValueError(f"linear_fp8: out must be a contiguous {dt} tensor of shape {shape}")
-        if workspace is None:
-            workspace = torch.zeros(256, dtype=torch.uint8, device=x.device)
+    if out is None:
+        if epi == EPI_F32_RESID:
+            raise ValueError("EPI_F32_RESID needs `out` (updated in place)")
+        out = _new(stream, shape, dt, x)
+    elif out.dtype is not dt or out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"linear_fp8: out must be a contiguous {dt} tensor of shape {shape}")
+    if workspace is None:
+        workspace = _new(stream, (256,), torch.uint8, x, zero=True)
     _check(lib.asr_op_linear_fp8(x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
                                  None if bias is None else bias.data_ptr(), M, N, K, epi, out.data_ptr(),
-                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+                                 workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev)))
     return out
 
 
 def _cross_operands(what, q, k, v, cu_q, cu_k, max_q, max_k, out, workspace):
-    """What the two cross-attention calls check alike -> (n_seg, max_q, max_k, H, Hkv)."""
-    import torch
-    _operands(what, q, k, v, cu_q, cu_k, out, workspace)
-    if q.dtype not in (torch.bfloat16, torch.float16) or k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+    """What the two cross-attention calls check alike -> (device, n_seg, max_q, max_k, H, Hkv, ldq, ldk, ldv)."""
+    torch = _t()
+    dev = _operands(what, q, k, v, cu_q, cu_k, out, workspace)
+    dt = q.dtype
+    if (dt is not torch.bfloat16 and dt is not torch.float16) or k.dtype is not dt or (v is not None and v.dtype is not dt):
         raise ValueError(f"{what}: q, k and v must be of one type, bf16 or f16")
-    _rows(what, q)
-    _rows(what, k)
-    if v is not None:
-        _rows(what, v, k.shape[1])
-    if q.shape[1] % 64 or k.shape[1] % 64 or not q.shape[1] or not k.shape[1] or q.shape[1] % k.shape[1] or (
-            v is not None and v.shape[0] != k.shape[0]):
+    ldq, ldk = _rows(what, q), _rows(what, k)
+    wq, wk = q.shape[1], k.shape[1]
+    ldv = 0 if v is None else _rows(what, v, wk)
+    if not wq or not wk or wq % 64 or wk % 64 or wq % wk or (v is not None and v.shape[0] != k.shape[0]):
         raise ValueError(f"{what}: need q [Tq, H * 64] and k, v [Tk, Hkv * 64] with H a multiple of Hkv")
     n_seg = cu_q.numel() - 1
-    if cu_q.dtype != torch.int32 or cu_k.dtype != torch.int32 or cu_q.dim() != 1 or tuple(cu_q.shape) != tuple(
-            cu_k.shape) or n_seg < 1 or not cu_q.is_contiguous() or not cu_k.is_contiguous():
+    if (cu_q.dtype is not torch.int32 or cu_k.dtype is not torch.int32 or cu_q.dim() != 1 or cu_q.shape != cu_k.shape
+            or n_seg < 1 or not cu_q.is_contiguous() or not cu_k.is_contiguous()):
         raise ValueError(f"{what}: cu_q and cu_k must be contiguous int32 [n_seg + 1]")
     if max_q is None:
         max_q = int((cu_q[1:] - cu_q[:-1]).max())
     if max_k is None:
         max_k = int((cu_k[1:] - cu_k[:-1]).max())
-    return n_seg, max_q, max_k, q.shape[1] // 64, k.shape[1] // 64
+    return dev, n_seg, max_q, max_k, wq // 64, wk // 64, ldq, ldk, ldv
 
 
 def cross_attention(q, k, v, cu_q, cu_k, max_q=None, max_k=None, out=None, workspace=None, stream=None,
@@ -577,22 +597,23 @@ def cross_attention(q, k, v, cu_q, cu_k, max_q=None, max_k=None, out=None, works
     """q CUDA [Tq, H*64], k and v CUDA [Tk, Hkv*64] (bf16 or f16, rows may be strided: a layer's columns of a
     product over all layers), cu_q / cu_k int32 CUDA [n_seg+1] -> [Tq, H*64] (asr_op_cross_attention).  Without
     max_q / max_k they are read from the device (a synchronisation).  Rows outside every segment are not
-    written (out keeps what it held).  workspace: a zeroed CUDA tensor of
-    asr_op_cross_attention_ws_size() bytes; with check the call synchronises and raises on bad offsets."""
-    import torch
-    n_seg, max_q, max_k, H, Hkv = _cross_operands("cross_attention", q, k, v, cu_q, cu_k, max_q, max_k, out, workspace)
-    with _allocating(stream):
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif out.dtype != q.dtype or out.shape != q.shape or (out.stride(1) != 1 and out.shape[1] > 1):
-            raise ValueError("cross_attention: out must be like q")
-        if workspace is None:
-            workspace = torch.zeros(256, dtype=torch.uint8, device=q.device)
-    st = _stream(stream)
-    _check(lib.asr_op_cross_attention(q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
-                                      cu_q.data_ptr(), cu_k.data_ptr(), n_seg, max_q, max_k, q.shape[0], k.shape[0], H,
-                                      Hkv, 2 if q.dtype == torch.float16 else 0, out.data_ptr(), out.stride(0),
-                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(), st))
+    written (out keeps what it held).  workspace: a zeroed CUDA tensor of asr_op_cross_attention_ws_size()
+    bytes; with check the call synchronises and raises on bad offsets."""
+    torch = _t()
+    dev, n_seg, max_q, max_k, H, Hkv, ldq, ldk, ldv = _cross_operands("cross_attention", q, k, v, cu_q, cu_k, max_q,
+                                                                      max_k, out, workspace)
+    if out is None:
+        out = _new(stream, q.shape, q.dtype, q)
+    elif out.dtype is not q.dtype or out.shape != q.shape:
+        raise ValueError("cross_attention: out must be like q")
+    ldo = _rows("cross_attention", out)
+    if workspace is None:
+        workspace = _new(stream, (256,), torch.uint8, q, zero=True)
+    st = _raw_stream(stream, dev)
+    _check(lib.asr_op_cross_attention(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, cu_q.data_ptr(),
+                                      cu_k.data_ptr(), n_seg, max_q, max_k, q.shape[0], k.shape[0], H, Hkv,
+                                      2 if q.dtype is torch.float16 else 0, out.data_ptr(), ldo, workspace.data_ptr(),
+                                      workspace.nbytes, st))
     if check:
         _check(lib.asr_op_cross_attention_check(workspace.data_ptr(), st))
     return out
@@ -604,31 +625,34 @@ def cross_attention_weights(q, k, cu_q, cu_k, max_q=None, max_k=None, heads=None
     [len(heads), Tq, max_k], columns past a segment's states zero (asr_op_cross_attention_weights).  out: such a
     tensor with contiguous columns and equally spaced rows; else the result is a view of rows padded to whole
     32 bytes."""
-    import torch
-    n_seg, max_q, max_k, H, Hkv = _cross_operands("cross_attention_weights", q, k, None, cu_q, cu_k, max_q, max_k, out,
-                                                  workspace)
+    torch = _t()
+    what = "cross_attention_weights"
+    dev, n_seg, max_q, max_k, H, Hkv, ldq, ldk, _ = _cross_operands(what, q, k, None, cu_q, cu_k, max_q, max_k, out,
+                                                                    workspace)
     Tq = q.shape[0]
-    with _allocating(stream):
-        if heads is None:
-            heads = torch.arange(H, dtype=torch.int32, device=q.device)
-        _operands("cross_attention_weights", heads)
-        if heads.dtype != torch.int32 or heads.dim() != 1 or not heads.is_contiguous():
-            raise ValueError("cross_attention_weights: heads must be a contiguous int32 vector")
-        n = heads.numel()
-        if out is None:
-            ldw = -(-max_k // 8) * 8
-            out = torch.empty((n, Tq, ldw), dtype=torch.float32, device=q.device)[:, :, :max_k]
-        elif out.dtype != torch.float32 or tuple(out.shape) != (n, Tq, max_k) or (out.stride(2) != 1 and max_k > 1) or (
-                n > 1 and out.stride(0) != Tq * out.stride(1)):
-            raise ValueError("cross_attention_weights: out must be float32 [len(heads), Tq, max_k] with equally spaced rows")
-        if workspace is None:
-            workspace = torch.zeros(256, dtype=torch.uint8, device=q.device)
-    st = _stream(stream)
-    _check(lib.asr_op_cross_attention_weights(q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0), cu_q.data_ptr(),
-                                              cu_k.data_ptr(), n_seg, max_q, max_k, Tq, k.shape[0], H, Hkv,
-                                              2 if q.dtype == torch.float16 else 0, heads.data_ptr(), n, out.data_ptr(),
-                                              out.stride(1), workspace.data_ptr(),
-                                              workspace.numel() * workspace.element_size(), st))
+    if heads is None:
+        n, hp = H, None
+    elif heads.get_device() != dev or heads.dtype is not torch.int32 or heads.dim() != 1 or not heads.is_contiguous():
+        raise ValueError(f"{what}: heads must be a contiguous int32 vector on the current CUDA device")
+    else:
+        n, hp = heads.numel(), heads.data_ptr()
+    if out is None:
+        ldw = -(-max_k // 8) * 8
+        out = _new(stream, (n, Tq, ldw), torch.float32, q)
+        if ldw != max_k:
+            out = out[:, :, :max_k]
+    else:
+        if out.dtype is not torch.float32 or out.shape != (n, Tq, max_k) or (out.stride(2) != 1 and max_k > 1) or (
+                n > 1 and Tq > 1 and out.stride(0) != Tq * out.stride(1)):
+            raise ValueError(f"{what}: out must be float32 [len(heads), Tq, max_k] with equally spaced rows")
+        ldw = out.stride(1) if Tq > 1 else out.stride(0) if n > 1 else max_k
+    if workspace is None:
+        workspace = _new(stream, (256,), torch.uint8, q, zero=True)
+    st = _raw_stream(stream, dev)
+    _check(lib.asr_op_cross_attention_weights(q.data_ptr(), ldq, k.data_ptr(), ldk, cu_q.data_ptr(), cu_k.data_ptr(),
+                                              n_seg, max_q, max_k, Tq, k.shape[0], H, Hkv,
+                                              2 if q.dtype is torch.float16 else 0, hp, n, out.data_ptr(),
+                                              ldw, workspace.data_ptr(), workspace.nbytes, st))
     if check:
         _check(lib.asr_op_cross_attention_check(workspace.data_ptr(), st))
     return out

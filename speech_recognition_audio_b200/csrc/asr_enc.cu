@@ -1983,8 +1983,8 @@ asr_status asr_op_cross_attention_weights(const void* q, int64_t ldq, const void
   const asr_status r = xattn_args("cross_attention_weights", a, q, ldq, k, ldk, nullptr, 0, cu_q, cu_k, n_seg, max_q,
                                   max_k, Tq, Tk, H, Hkv, dtype, weights, ldw, ws, ws_bytes);
   if (r != ASR_OK) return r;
-  if (!heads || n_sel <= 0 || n_sel > 65535 || ldw < max_k || (reinterpret_cast<uintptr_t>(weights) & 3))
-    return fail(nullptr, ASR_E_INVAL, "cross_attention_weights: need heads and ldw >= max_k");
+  if (n_sel <= 0 || n_sel > 65535 || (!heads && n_sel != H) || ldw < max_k || (reinterpret_cast<uintptr_t>(weights) & 3))
+    return fail(nullptr, ASR_E_INVAL, "cross_attention_weights: need n_sel heads (or all H) and ldw >= max_k");
   if (Tq == 0 || max_q == 0 || max_k == 0) return ASR_OK;
   a.heads = heads;
   a.width = max_k;

@@ -651,7 +651,8 @@ cudaError_t run_fp8(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMa
                     const Fp8Params& f, int grid, cudaStream_t st) {
   using S = Fp8Shape<BN, epi_wide<EPI>()>;
   auto k = gemm_fp8_tc_kernel<BN, EPI, KIND>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = set_smem_once(k, S::SMEM_BYTES, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3(grid), dim3(S::THREADS), S::SMEM_BYTES, st, a, b, o, p, f);
 }

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <utility>
 
 #include "common.cuh"
@@ -44,6 +45,21 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, siz
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Sets a kernel's dynamic shared memory limit (and the largest carveout) once
+// per device; `done` is the caller's own mask of devices, one per kernel.
+template <typename... KArgs>
+cudaError_t set_smem_once(void (*kernel)(KArgs...), size_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) & bit))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Tables of the log-mel kernel, built on the device by launch_mel_tables.

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(32 * XS_WARPS, 3) xattn_rows_kernel(const Xatt
 // sum, joined over warps and the blocks of the cluster; then the scores again,
 // written as probabilities in 32 bits.  A row's 8 keys of a step are one
 // 32-byte sector of the output.
-constexpr int XW_WARPS = 8, XW_KEYS = 16;
+constexpr int XW_WARPS = 8, XW_KEYS = 32;
 
 template <int KIND, int RT>
 __global__ void __launch_bounds__(32 * XW_WARPS, 2) xattn_weights_kernel(const XattnArgs a) {
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(32 * XW_WARPS, 2) xattn_weights_kernel(const X
   const int S = a.splits, seg = blockIdx.x / S, rank = blockIdx.x - seg * S;
   const int row0 = blockIdx.y * 16 * RT;
   const Segment s = load_segment(a, seg, tid == 0);
-  const int h = __ldg(a.heads + blockIdx.z);
+  const int h = a.heads ? __ldg(a.heads + blockIdx.z) : blockIdx.z;
   const bool head_ok = h >= 0 && h < a.H;
   if (!head_ok && tid == 0) atomicCAS(a.status, 0, DEV_BAD_SEGMENT);
   if (!s.ok || !head_ok || row0 >= s.lq) return;  // the same for every block of the cluster
@@ -282,38 +282,51 @@ __global__ void __launch_bounds__(32 * XW_WARPS, 2) xattn_weights_kernel(const X
   for (int r = 0; r < RT; ++r) m[r][0] = m[r][1] = -INFINITY, l[r][0] = l[r][1] = 0.f;
   auto load_k = [&](int j0, uint4 (*kf)[2]) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < 4; ++u) {
       const int j = j0 + 8 * u + g;
 #pragma unroll
       for (int c = 0; c < 2; ++c) kf[u][c] = ld16(kp + (long long)j * a.ldk + 32 * c, j < hi);
     }
   };
-  for (int j0 = lo + warp * XW_KEYS; j0 < hi; j0 += XW_WARPS * XW_KEYS) {
-    uint4 kf[2][2];
-    load_k(j0, kf);
+  constexpr int STEP = XW_WARPS * XW_KEYS;
+  uint4 kf[4][2];
+  load_k(lo + warp * XW_KEYS, kf);
+  for (int j0 = lo + warp * XW_KEYS; j0 < hi; j0 += STEP) {
+    uint4 kn[4][2];
+    if (RT == 1) load_k(j0 + STEP, kn);  // registers for the next step's keys only beside few rows
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      float c[2][4];
+      float c[4][4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        scores8<KIND>(c[u], qf[r], kf[u][0], kf[u][1]);
+      for (int u = 0; u < 4; ++u) scores8<KIND>(c[u], qf[r], kf[u][0], kf[u][1]);
+      if (j0 + XW_KEYS > hi) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (j0 + 8 * u + 2 * t + (i & 1) >= hi) c[u][i] = -INFINITY;
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (j0 + 8 * u + 2 * t + (i & 1) >= hi) c[u][i] = -INFINITY;
       }
       // per lane: its four lanes of a row are joined once at the end
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
-        const float mx = fmaxf(fmaxf(c[0][2 * hh], c[0][2 * hh + 1]), fmaxf(c[1][2 * hh], c[1][2 * hh + 1]));
+        float mx = fmaxf(c[0][2 * hh], c[0][2 * hh + 1]);
+#pragma unroll
+        for (int u = 1; u < 4; ++u) mx = fmaxf(mx, fmaxf(c[u][2 * hh], c[u][2 * hh + 1]));
         const float mn = fmaxf(m[r][hh], mx * kScaleLog2), sh = shift_of(mn);
         float sum = 0.f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
           for (int i = 2 * hh; i < 2 * hh + 2; ++i) sum += ex2_approx(fmaf(c[u][i], kScaleLog2, -sh));
         l[r][hh] = l[r][hh] * ex2_approx(m[r][hh] - sh) + sum;
         m[r][hh] = mn;
       }
+    }
+    if (RT == 1) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) kf[u][0] = kn[u][0], kf[u][1] = kn[u][1];
+    } else {
+      load_k(j0 + STEP, kf);
     }
   }
 #pragma unroll
@@ -364,32 +377,35 @@ __global__ void __launch_bounds__(32 * XW_WARPS, 2) xattn_weights_kernel(const X
     }
   float* out = reinterpret_cast<float*>(a.out) + ((long long)blockIdx.z * a.Tq + s.q0 + row0) * a.ldo;
   const bool pairs = ((reinterpret_cast<uintptr_t>(a.out) & 7) | (a.ldo & 1)) == 0;  // rows of whole 8 bytes
-  for (int j0 = lo + warp * XW_KEYS; j0 < end; j0 += XW_WARPS * XW_KEYS) {
-    uint4 kf[2][2];
-    load_k(j0, kf);
+  load_k(lo + warp * XW_KEYS, kf);
+  for (int j0 = lo + warp * XW_KEYS; j0 < end; j0 += STEP) {
+    const bool whole = pairs && j0 + XW_KEYS <= hi;
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int r = 0; r < RT; ++r) {
+      float c[4][4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float c[4];
-        scores8<KIND>(c, qf[r], kf[u][0], kf[u][1]);
-        const int j = j0 + 8 * u + 2 * t;
+      for (int u = 0; u < 4; ++u) scores8<KIND>(c[u], qf[r], kf[u][0], kf[u][1]);
+      if (RT == 1 || r == RT - 1) load_k(j0 + STEP, kf);
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int row = 16 * r + g + 8 * hh;
-          if (row0 + row >= s.lq) continue;
+      for (int hh = 0; hh < 2; ++hh) {
+        const int row = 16 * r + g + 8 * hh;
+        if (row0 + row >= s.lq) continue;
+        float* dst = out + row * a.ldo + j0 + 2 * t;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
           float2 p;
-          p.x = j < hi ? ex2_approx(fmaf(c[2 * hh], kScaleLog2, -sh[r][hh])) * inv[r][hh] : 0.f;
-          p.y = j + 1 < hi ? ex2_approx(fmaf(c[2 * hh + 1], kScaleLog2, -sh[r][hh])) * inv[r][hh] : 0.f;
-          float* dst = out + row * a.ldo + j;
-          if (pairs && j + 1 < end) {
-            *reinterpret_cast<float2*>(dst) = p;
+          p.x = ex2_approx(fmaf(c[u][2 * hh], kScaleLog2, -sh[r][hh])) * inv[r][hh];
+          p.y = ex2_approx(fmaf(c[u][2 * hh + 1], kScaleLog2, -sh[r][hh])) * inv[r][hh];
+          if (whole) {
+            *reinterpret_cast<float2*>(dst + 8 * u) = p;
           } else {
-            if (j < end) dst[0] = p.x;
-            if (j + 1 < end) dst[1] = p.y;
+            const int j = j0 + 8 * u + 2 * t;
+            if (j < end) dst[8 * u] = j < hi ? p.x : 0.f;
+            if (j + 1 < end) dst[8 * u + 1] = j + 1 < hi ? p.y : 0.f;
           }
         }
       }
+    }
   }
 }
 

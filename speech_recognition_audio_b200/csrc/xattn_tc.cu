@@ -379,9 +379,8 @@ template <int KIND>
 static cudaError_t launch_tiles(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const XattnArgs& a,
                                 int n_seg, cudaStream_t st) {
   auto kern = xattn_tiles_kernel<KIND>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XT_SMEM);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = set_smem_once(kern, XT_SMEM, done);
   if (e != cudaSuccess) return e;
   const int q_blocks = (a.max_q + 127) / 128;
   return launch_cluster(kern, dim3(n_seg * q_blocks * a.splits, a.H), XT_THREADS, XT_SMEM, a.splits, st, q, k, v, a, q_blocks);
