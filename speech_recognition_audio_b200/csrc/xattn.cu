@@ -419,6 +419,7 @@ cudaError_t launch_xattn(XattnArgs a, int n_seg, int max_k, bool f16, int num_sm
 }
 
 cudaError_t launch_xattn_weights(XattnArgs a, int n_seg, int n_sel, bool f16, int num_sms, cudaStream_t st) {
+  if (a.max_q > 32 && a.Tk > 0) return launch_xattn_weights_tiles(a, n_seg, n_sel, f16, st);
   const bool wide = a.max_q > 16;
   const int rows = wide ? 64 : 16, tiles = (a.max_q + rows - 1) / rows;
   a.splits = pick_splits((long long)n_seg * tiles * n_sel, a.width, XW_WARPS * XW_KEYS, num_sms);

@@ -396,4 +396,244 @@ cudaError_t launch_xattn_tiles(XattnArgs a, int n_seg, int max_k, bool f16, int 
   return f16 ? launch_tiles<KIND_F16>(q, k, v, a, n_seg, st) : launch_tiles<KIND_BF16>(q, k, v, a, n_seg, st);
 }
 
+// Attention weights of many rows: the scores of a 128-row tile of one
+// (segment, selected head) from the tensor cores, twice over the states.  The
+// first pass keeps each thread's running maximum and sum (its row, its half of
+// every tile), joined over the two halves once at its end; the second turns
+// the same scores into probabilities, staged as 32 x 32 boxes and written by
+// TMA.  mma.sync, whose rate here is about an eighth of tcgen05's, bounded
+// the 64-row form of this (402 us for 448 rows x 1500 states x 10 heads x 32
+// segments, 142 us of them the output's bytes).
+namespace {
+constexpr int XWT_KS = 2, XWT_SK = XT_TILE, XWT_BUF = XWT_SK + XWT_KS * XT_TILE, XWT_RED = XWT_BUF + 8 * 4096;
+constexpr int XWT_BARS = XWT_RED + 2 * 128 * 8;
+enum { WB_Q = 0, WB_KF, WB_KE = WB_KF + XWT_KS, WB_SF = WB_KE + XWT_KS, WB_SE = WB_SF + 2, WB_DRAIN = WB_SE + 2, WB_COUNT };
+constexpr int XWT_SMEM = 1024 + XWT_BARS + 8 * WB_COUNT + 16;
+static_assert(2 * (XWT_SMEM + 1024) <= 228 * 1024, "two blocks per SM");
+}  // namespace
+
+template <int KIND>
+__global__ void __launch_bounds__(320, 2)
+    xattn_weights_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                               const __grid_constant__ CUtensorMap tm_out, const XattnArgs a, int q_blocks, int out_tma) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int failed;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + XWT_BARS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + WB_COUNT);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if (tid == 0) {
+    failed = 0;
+    for (int i = 0; i < WB_COUNT; ++i) mbar_init(&bar[i], i == WB_SE || i == WB_SE + 1 ? 8 : 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+  }
+  if (warp == XT_MMA_WARP) {
+    tmem_alloc(tmem_slot, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  const int seg = blockIdx.x / q_blocks, row0 = (blockIdx.x - seg * q_blocks) * 128, sel = blockIdx.y;
+  const Segment s = load_segment(a, seg, tid == 0);
+  const int h = a.heads ? __ldg(a.heads + sel) : sel;
+  const bool head_ok = h >= 0 && h < a.H;
+  if (!head_ok && tid == 0) atomicCAS(a.status, 0, DEV_BAD_SEGMENT);
+  const bool live = s.ok && head_ok && row0 < s.lq;
+  const int nk = (s.lk + 127) / 128;
+
+  if (live && nk > 0 && warp == XT_TMA_WARP) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bar[WB_Q], XT_TILE);
+      tma_load_2d(sm, &tm_q, &bar[WB_Q], h * 64, s.q0 + row0);
+      int n = 0;
+      for (; n < 2 * nk; ++n) {
+        const int ks = n % XWT_KS, j = n < nk ? n : n - nk;
+        if (!mbar_wait(&bar[WB_KE + ks], ((n / XWT_KS) & 1) ^ 1, a.limit_ns, &failed, DEV_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(&bar[WB_KF + ks], XT_TILE);
+        tma_load_2d(sm + XWT_SK + ks * XT_TILE, &tm_k, &bar[WB_KF + ks], h / a.G * 64, s.k0 + j * 128);
+      }
+      // every issued load lands before the block exits
+      mbar_wait(&bar[WB_Q], 0, kDrainLimitNs, nullptr, 0);
+      for (int i = max(0, n - XWT_KS); i < n; ++i)
+        mbar_wait(&bar[WB_KF + i % XWT_KS], (i / XWT_KS) & 1, kDrainLimitNs, nullptr, 0);
+    }
+  } else if (live && nk > 0 && warp == XT_MMA_WARP) {
+    const uint32_t idesc = idesc_kind_f32(KIND, 128, 128);
+    const uint64_t qd = sw128_kmajor_desc(smem_u32(sm)), kd = sw128_kmajor_desc(smem_u32(sm + XWT_SK));
+    auto wait = [&](int b, int n) {
+      return __all_sync(0xffffffffu, mbar_wait(&bar[b], n & 1, a.limit_ns, &failed, DEV_TIMEOUT_MMA)) != 0;
+    };
+    bool ok = wait(WB_Q, 0);
+    for (int n = 0; n < 2 * nk && ok; ++n) {
+      const int b = n & 1, ks = n % XWT_KS;
+      if (!(ok = wait(WB_KF + ks, n / XWT_KS) && wait(WB_SE + b, (n >> 1) ^ 1))) break;
+      tc_fence_after();
+      tc_scores_warp(tmem + 128 * b, qd, kd + ks * (XT_TILE >> 4), idesc);
+      tc_commit_warp(&bar[WB_SF + b]);
+      tc_commit_warp(&bar[WB_KE + ks]);
+    }
+    // all issued MMAs complete before tensor memory is released
+    tc_commit_warp(&bar[WB_DRAIN]);
+    mbar_wait(&bar[WB_DRAIN], 0, kDrainLimitNs, nullptr, 0);
+  } else if (live && warp < XT_TMA_WARP) {
+    const int q = warp & 3, hh = warp >> 2, row = 32 * q + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * q) << 16) + 64 * hh;
+    float m = -INFINITY, l = 0.f, sh = 0.f, inv = 0.f;
+    // After a failed wait the loops run on without waiting, so that the two
+    // warps of a pair meet the same barrier.
+    bool ok = true;
+    auto scores = [&](int n, float* v) {
+      ok = ok && mbar_wait(&bar[WB_SF + (n & 1)], (n >> 1) & 1, a.limit_ns, &failed, DEV_TIMEOUT_EPILOGUE);
+      tc_fence_after();
+      tmem_ld32(trow + 128 * (n & 1), v);
+      tmem_ld32(trow + 128 * (n & 1) + 32, v + 32);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[WB_SE + (n & 1)]);
+    };
+    for (int j = 0; j < nk; ++j) {
+      float v[64];
+      scores(j, v);
+      const int kv = s.lk - j * 128 - 64 * hh;  // states of this half
+      if (kv < 64) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (c >= kv) v[c] = -INFINITY;
+      }
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < 64; c += 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], fmaxf(v[c + 2 * i], v[c + 2 * i + 1]));
+      }
+      const float mn = fmaxf(m, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * kScaleLog2);
+      sh = shift_of(mn);
+      l *= ex2_approx(m - sh);
+      m = mn;
+      const float2 scale2 = make_float2(kScaleLog2, kScaleLog2), shift2 = make_float2(-sh, -sh);
+      float2 s2[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        const float2 x = fma2(make_float2(v[c], v[c + 1]), scale2, shift2);
+        s2[(c >> 1) & 3] = add2(s2[(c >> 1) & 3], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+      }
+      l += ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y));
+    }
+    if (nk > 0) {
+      float2* red = reinterpret_cast<float2*>(sm + XWT_RED);
+      red[hh * 128 + row] = make_float2(m, l);
+      pair_sync(q);
+      const float2 x = red[row], y = red[128 + row];
+      sh = shift_of(fmaxf(x.x, y.x));
+      inv = 1.0f / (x.y * ex2_approx(x.x - sh) + y.y * ex2_approx(y.x - sh));
+    }
+    uint8_t* buf = sm + XWT_BUF + warp * 4096;
+    const int rows = s.lq - row0 - 32 * q;  // valid rows of this warp, if fewer than 32
+    const long long orow = (long long)sel * a.Tq + s.q0 + row0 + 32 * q;
+    const bool vec = ((reinterpret_cast<uintptr_t>(a.out) & 15) | (a.ldo & 3)) == 0;
+    for (int j = 0; j * 128 + 64 * hh < a.width && rows > 0; ++j) {
+      float v[64];
+      if (j < nk) {
+        scores(nk + j, v);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) v[c] = 0.f;  // columns past the states: zeros below
+      }
+      const int kv = s.lk - j * 128 - 64 * hh;
+      const float2 scale2 = make_float2(kScaleLog2, kScaleLog2), shift2 = make_float2(-sh, -sh), inv2 = make_float2(inv, inv);
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        const float2 x = fma2(make_float2(v[c], v[c + 1]), scale2, shift2);
+        const float2 p = mul2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), inv2);
+        v[c] = p.x, v[c + 1] = p.y;
+      }
+      if (kv < 64) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (c >= kv) v[c] = 0.f;
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int x0 = j * 128 + 64 * hh + 32 * b;
+        if (x0 >= a.width) break;
+        if (lane == 0) bulk_wait_read0();  // the box stored last has been read
+        __syncwarp();
+        float4* dst = reinterpret_cast<float4*>(buf + lane * 128);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          dst[k ^ (lane & 7)] = make_float4(v[32 * b + 4 * k], v[32 * b + 4 * k + 1], v[32 * b + 4 * k + 2], v[32 * b + 4 * k + 3]);
+        if (out_tma && rows >= 32) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tm_out, buf, x0, static_cast<int>(orow));
+            bulk_commit();
+          }
+        } else {
+          // rows of the next segment follow inside the box, or rows are not
+          // whole 16 bytes: eight lanes a row
+          __syncwarp();
+#pragma unroll 1
+          for (int r = lane >> 3; r < min(32, rows); r += 4) {
+            const float4 f = reinterpret_cast<const float4*>(buf + r * 128)[(lane & 7) ^ (r & 7)];
+            const int x = x0 + 4 * (lane & 7);
+            float* o = reinterpret_cast<float*>(a.out) + (orow + r) * a.ldo + x;
+            if (vec && x + 4 <= a.width) {
+              *reinterpret_cast<float4*>(o) = f;
+            } else {
+              if (x < a.width) o[0] = f.x;
+              if (x + 1 < a.width) o[1] = f.y;
+              if (x + 2 < a.width) o[2] = f.z;
+              if (x + 3 < a.width) o[3] = f.w;
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    // a warp without rows still gives back the scores of the second pass
+    if (rows <= 0) {
+      for (int j = 0; j < nk; ++j) {
+        ok = ok && mbar_wait(&bar[WB_SF + ((nk + j) & 1)], ((nk + j) >> 1) & 1, a.limit_ns, &failed, DEV_TIMEOUT_EPILOGUE);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[WB_SE + ((nk + j) & 1)]);
+      }
+    } else if (nk > 0 && (nk - 1) * 128 + 64 * hh >= a.width) {
+      // (the last tile's second half lies past the width)
+      ok = ok && mbar_wait(&bar[WB_SF + ((2 * nk - 1) & 1)], ((2 * nk - 1) >> 1) & 1, a.limit_ns, &failed, DEV_TIMEOUT_EPILOGUE);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[WB_SE + ((2 * nk - 1) & 1)]);
+    }
+    if (lane == 0) bulk_wait0();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == XT_MMA_WARP) tmem_dealloc(tmem, 256);
+  if (tid == 0 && failed) atomicCAS(a.status, 0, failed);
+}
+
+cudaError_t launch_xattn_weights_tiles(XattnArgs a, int n_seg, int n_sel, bool f16, cudaStream_t st) {
+  CUtensorMap q, k, o;
+  if (!make_tmap_bf16(&q, a.q, a.Tq, 64ULL * a.H, a.ldq, 128) ||
+      !make_tmap_bf16(&k, a.k, a.Tk, 64ULL * (a.H / a.G), a.ldk, 128))
+    return cudaErrorInvalidValue;
+  const bool tma = n_sel * a.Tq < (1LL << 31) && make_tmap_out(&o, a.out, n_sel * a.Tq, a.width, a.ldo, true);
+  if (!tma) o = k;
+  const int q_blocks = (a.max_q + 127) / 128;
+  auto kern = f16 ? xattn_weights_tiles_kernel<KIND_F16> : xattn_weights_tiles_kernel<KIND_BF16>;
+  static std::atomic<unsigned long long> done[2] = {{0}, {0}};
+  const cudaError_t e = set_smem_once(kern, XWT_SMEM, done[f16]);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(kern, dim3(n_seg * q_blocks, n_sel), 320, XWT_SMEM, 1, st, q, k, o, a, q_blocks, (int)tma);
+}
+
 }  // namespace asr
