@@ -11,13 +11,17 @@
 //             the next tile's product runs under the exponentials.
 // Tensor memory: S 128, P 64, O 64 columns, none shared.
 //
-// What bounds it is the exponentials: 16 per clock and SM against 4096 products,
-// so a tile of 128 x 128 costs 1024 clocks of them and 512 of the tensor pipe.
-// A warp's own chain (wait, read, maximum, exponentials, write) is about twice
-// as long as its exponentials, so it takes four softmax warps per scheduler
-// to keep that unit busy.  Measured on 2240 rows x 1500 states x 12 heads x
-// 32 segments: two per scheduler (one thread a row, two tiles a block) 617 us,
-// with the tiles' exponentials taking turns 762.
+// What bounds it is the softmax: 16 exponentials per clock and SM against 4096
+// products, so a tile of 128 x 128 costs 1024 clocks of them and 512 of the
+// tensor pipe, and a warp's own chain (wait, read, maximum, exponentials,
+// write) is about twice as long as its exponentials.  Four softmax warps per
+// scheduler keep that unit about half busy; the two warps a block puts on a
+// scheduler move in step, which is why it is not more.  2240 rows x 1500 states
+// x 12 heads x 32 segments (330 GFLOP, 1.29e9 exponentials = 277 us at 1965
+// MHz): 605 us.  Measured on the way there: single-lane issue with waits behind
+// a call 868; one thread a row and two tiles a block 617, with the tiles'
+// exponentials taking turns 762; exponentials ahead of the maximum, repeated
+// where it moved, 615.
 //
 // The running maximum used for the exponentials moves only when a row's
 // maximum exceeds it by more than 2^8 (then O and the sum are rescaled), so
@@ -236,72 +240,52 @@ __global__ void __launch_bounds__(XT_THREADS, 2)
           fence_proxy_async_smem();
         }
       }
-      // The row's maximum over both halves (scaled).  Buffers alternate: a warp
-      // writes one again only after its partner has passed the next barrier,
-      // having read it.
-      float* rbuf = red + (j & 1) * 256;
-      auto row_max = [&](float mine) {
-        rbuf[hh * 128 + row] = mine;
-        pair_sync(q);
-        return fmaxf(rbuf[row], rbuf[128 + row]) * kScaleLog2;
-      };
-      // P = 2^(S scale - shift) into tensor memory; this half's sum, and its
-      // maximum formed beside the exponentials (each fills the other's waits)
-      float hm, sum;
-      auto exponentials = [&](bool wait_free) {
-        const float sh = shift_of(m_used);
-        const float2 scale2 = make_float2(kScaleLog2, kScaleLog2), shift2 = make_float2(-sh, -sh);
-        float2 s2[2] = {{0.f, 0.f}, {0.f, 0.f}};
-        float m2[2] = {-INFINITY, -INFINITY};
+      // The row's maximum over both halves.  Buffers alternate: a warp writes
+      // one again only after its partner has passed the next barrier, having
+      // read it.
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          float pk[16];
+      for (int c = 0; c < 64; c += 8) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 v = make_float2(sv[c + i], sv[c + i + 1]);
-            const float2 x = fma2(v, scale2, shift2);
-            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            m2[(i >> 1) & 1] = fmaxf(m2[(i >> 1) & 1], fmaxf(v.x, v.y));
-            s2[(i >> 1) & 1] = add2(s2[(i >> 1) & 1], p);
-            pk[i >> 1] = __uint_as_float(pack2_16<KIND>(p.x, p.y));
-          }
-          if (c == 0 && wait_free) wait(XB_OD, j - 1);  // P and O are free once the previous product is complete
-          tmem_st16(trow + XT_P + 32 * hh + c / 2, pk);
-        }
-        hm = fmaxf(m2[0], m2[1]);
-        sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
-      };
-      // Past the first tile the exponentials go ahead with the maximum so far.
-      float mt;
-      if (j == 0) {
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 64; ++c) m4[c & 3] = fmaxf(m4[c & 3], sv[c]);
-        m_used = mt = row_max(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-        exponentials(false);
-      } else {
-        exponentials(true);
-        mt = row_max(hm);
+        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], fmaxf(sv[c + 2 * i], sv[c + 2 * i + 1]));
       }
+      float* rbuf = red + (j & 1) * 256;
+      rbuf[hh * 128 + row] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      pair_sync(q);
+      const float mt = fmaxf(rbuf[row], rbuf[128 + row]) * kScaleLog2;
       const bool grow = mt > m_used + kRescaleLog2;
       if (__any_sync(0xffffffffu, grow)) {
-        // a row's maximum moved: O and the sum are rescaled, the tile's
-        // exponentials taken again
         const float corr = grow ? ex2_approx(m_used - mt) : 1.0f;  // 0 where there was no maximum yet
         if (grow) m_used = mt;
         lsum *= corr;
+        if (j > 0) {
+          wait(XB_OD, j - 1);  // O is still once the previous product is complete
 #pragma unroll
-        for (int c = 0; c < 32; c += 16) {
-          float ov[16];
-          tmem_ld16(trow + XT_O + 32 * hh + c, ov);
-          tmem_ld_wait();
+          for (int c = 0; c < 32; c += 16) {
+            float ov[16];
+            tmem_ld16(trow + XT_O + 32 * hh + c, ov);
+            tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) ov[i] *= corr;
-          tmem_st16(trow + XT_O + 32 * hh + c, ov);
+            for (int i = 0; i < 16; ++i) ov[i] *= corr;
+            tmem_st16(trow + XT_O + 32 * hh + c, ov);
+          }
         }
-        exponentials(false);
       }
-      lsum += sum;
+      const float sh = shift_of(m_used);
+      const float2 scale2 = make_float2(kScaleLog2, kScaleLog2), shift2 = make_float2(-sh, -sh);
+      float2 s2[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+      float pk[32];
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        const float2 x = fma2(make_float2(sv[c], sv[c + 1]), scale2, shift2);
+        const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        s2[(c >> 1) & 3] = add2(s2[(c >> 1) & 3], p);
+        pk[c >> 1] = __uint_as_float(pack2_16<KIND>(p.x, p.y));
+      }
+      if (j > 0) wait(XB_OD, j - 1);  // P is free once the previous product has read it
+      tmem_st16(trow + XT_P + 32 * hh, pk);
+      tmem_st16(trow + XT_P + 32 * hh + 16, pk + 16);
+      lsum += ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y));
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
