@@ -220,8 +220,9 @@ asr_status asr_op_linear_fp8(const void* x, const void* xs, const void* w, const
  *         synchronises the stream and turns the word into ASR_OK, ASR_E_INVAL
  *         or ASR_E_DEVICE_TIMEOUT.
  * Limits: H % Hkv == 0, strides multiples of 8 elements and at least the row
- * width, pointers 16-byte aligned (ASR_E_INVAL); Hkv <= 65535 and max_q * G <=
- * 1048560 (ASR_E_UNSUPPORTED).  Tq == 0 does nothing.
+ * width, pointers 16-byte aligned (ASR_E_INVAL); H <= 65535, max_q * G <=
+ * 1048560 and n_seg * ceil(max_q / 128) < 2^28 (ASR_E_UNSUPPORTED).  Tq == 0 or
+ * max_q == 0 does nothing.
  * Results do not depend on timing: the parts of a split row are joined in a
  * fixed order. */
 size_t asr_op_cross_attention_ws_size(void);

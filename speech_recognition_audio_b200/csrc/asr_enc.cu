@@ -1925,8 +1925,9 @@ static asr_status xattn_args(const char* who, XattnArgs& a, const void* q, int64
     return fail(nullptr, ASR_E_INVAL, "%s: bad arguments", who);
   if (!ws || ws_bytes < asr_op_cross_attention_ws_size() || (reinterpret_cast<uintptr_t>(ws) & 3))
     return fail(nullptr, ASR_E_WORKSPACE, "%s: workspace too small", who);
-  if (Tq > 0x7FFFFFFF || Tk > 0x7FFFFFFF || Hkv > 65535 || n_seg > 0x7FFFFFFF / 8 ||
-      (long long)max_q * (H / Hkv) > 16LL * 65535)
+  // grid dimensions: (segments x row tiles x splits, heads or row tiles, heads)
+  if (Tq > 0x7FFFFFFF || Tk > 0x7FFFFFFF || H > 65535 || (long long)max_q * (H / Hkv) > 16LL * 65535 ||
+      ((long long)max_q + 127) / 128 * 8 * n_seg > 0x7FFFFFFF)
     return fail(nullptr, ASR_E_UNSUPPORTED, "%s: sizes beyond the limits", who);
   const int64_t wq = 64LL * H, wk = 64LL * Hkv;
   if (Tq > 0 && (!q || !out || (reinterpret_cast<uintptr_t>(q) & 15) || ldq < wq || ldq % 8))

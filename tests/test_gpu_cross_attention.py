@@ -195,3 +195,139 @@ def test_weights_into_rows_of_odd_stride():
     got = sra.cross_attention_weights(qd, kd, cq, ck, max_k=61, out=buf[:, :, :61])
     ref = sra.cross_attention_weights(qd, kd, cq, ck)
     assert torch.equal(got, ref) and (buf[:, :, 61:] == 9).all()
+
+
+def test_bad_offsets_are_reported_and_leave_the_rest():
+    """Offsets outside the arrays, decreasing ones and segments longer than stated are refused by the kernels'
+    own bounds checks; the other segments are computed."""
+    for lq, max_q in (([4, 5], 5), ([60, 70], 70)):
+        q, k, v, cu_q, cu_k = _data(lq, [50, 60], 2, 2, "bf16", 20)
+        qd, kd, vd, cq, ck = _dev(q, k, v, cu_q, cu_k)
+        first = sra.cross_attention(qd, kd, vd, cq, ck)[:lq[0]].clone()
+        i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+        n = sum(lq)
+        for bad_q, bad_k, mq in ((cq, i32(0, 50, 111), max_q), (cq, i32(0, 50, 40), max_q), (i32(0, lq[0], n + 1), ck, max_q),
+                                 (i32(0, lq[0], lq[0] - 1), ck, max_q), (cq, ck, max_q - 1)):
+            out = torch.full_like(qd, 3.0)
+            ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+            with pytest.raises(sra.AsrError) as e:
+                sra.cross_attention(qd, kd, vd, bad_q, bad_k, mq, 60, out=out, workspace=ws)
+            assert e.value.code == 1 and int(ws.view(torch.int32)[0]) == 7
+            assert torch.equal(out[:lq[0]], first) and (out[lq[0]:] == 3).all()
+        w = sra.cross_attention_weights(qd, kd, cq, ck)
+        for heads, bad_k, mk in ((i32(0, 2), ck, 60), (i32(-1), ck, 60), (i32(0), i32(0, 50, 111), 60), (i32(0), ck, 59)):
+            with pytest.raises(sra.AsrError):
+                sra.cross_attention_weights(qd, kd, cq, bad_k, max_q, mk, heads=heads)
+        assert torch.equal(sra.cross_attention_weights(qd, kd, cq, ck), w)
+
+
+@pytest.mark.parametrize("lq,lk", [([1], [5000]), ([6], [5000]), ([20, 3], [700, 4000]), ([200], [5000]), ([300, 140], [64, 900])])
+def test_repeats_are_bit_identical_and_max_k_only_steers(lq, lk):
+    data = _data(lq, lk, 4, 2, "f16", 21)
+    dev = _dev(*data)
+    first = sra.cross_attention(*dev)
+    for _ in range(3):
+        assert torch.equal(sra.cross_attention(*dev), first)
+    for max_k in (0, 1, 100000):
+        check_attention(sra.cross_attention(*dev, max_q=max(lq), max_k=max_k), *data, "f16", max_k)
+    check_attention(sra.cross_attention(*dev, max_q=max(lq) + 300, max_k=max(lk)), *data, "f16", "max_q")
+
+
+@pytest.mark.parametrize("lq", [[3, 9], [40, 150]])
+def test_strided_queries_and_outputs(lq):
+    q, k, v, cu_q, cu_k = _data(lq, [300, 77], 4, 2, "bf16", 22)
+    qd, kd, vd, cq, ck = _dev(q, k, v, cu_q, cu_k)
+    wide = torch.full((sum(lq), 3 * 256), 5.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, 256:512] = qd
+    out = torch.full((sum(lq), 2 * 256), 5.0, dtype=torch.bfloat16, device="cuda")
+    sra.cross_attention(wide[:, 256:512], kd, vd, cq, ck, out=out[:, 256:])
+    assert torch.equal(out[:, 256:], sra.cross_attention(qd, kd, vd, cq, ck)) and (out[:, :256] == 5).all()
+    assert torch.equal(sra.cross_attention_weights(wide[:, 256:512], kd, cq, ck),
+                       sra.cross_attention_weights(qd, kd, cq, ck))
+
+
+@pytest.mark.parametrize("lq", [[2, 1], [70, 200]])
+def test_streams_and_graphs(lq):
+    """Captured and replayed on new inputs; on two streams at once with one workspace; on a stream that is
+    not the tensors' own."""
+    lk = [1500, 333]
+    sets = [_dev(*_data(lq, lk, 4, 4, "bf16", 30 + i)) for i in range(3)]
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    kw = dict(max_q=max(lq), max_k=max(lk), workspace=ws, check=False)
+    run = lambda s, **m: (sra.cross_attention(*s, **kw, **m),  # noqa: E731
+                          sra.cross_attention_weights(s[0], s[1], s[3], s[4], **kw, **m))
+    ref = [run(s) for s in sets]
+    torch.cuda.synchronize()
+    mine = tuple(t.clone() for t in sets[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(mine)
+    for i in (1, 2, 0):
+        for a, b in zip(mine, sets[i]):
+            a.copy_(b)
+        graph.replay()
+        assert torch.equal(got[0], ref[i][0])
+        for j, n in enumerate(lk):
+            rows = slice(sum(lq[:j]), sum(lq[:j + 1]))
+            assert torch.equal(got[1][:, rows], ref[i][1][:, rows])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [(i, run(sets[i], stream=streams[i])) for _ in range(5) for i in range(2)]
+    outs.append((2, run(sets[2], stream=streams[0].cuda_stream)))
+    torch.cuda.synchronize()
+    for i, (o, w) in outs:
+        assert torch.equal(o, ref[i][0]) and torch.equal(w, ref[i][1])
+    assert int(ws.view(torch.int32)[0]) == 0
+
+
+def test_no_rows_and_no_states_at_all():
+    q, k, v, cu_q, cu_k = _dev(*_data([5, 140], [1, 1], 2, 1, "bf16", 40))
+    none = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out = sra.cross_attention(q, k[:0], v[:0], cu_q, none)
+    assert (out == 0).all()
+    assert (sra.cross_attention_weights(q, k[:0], cu_q, none, max_k=9) == 0).all()
+    assert sra.cross_attention(q[:0], k, v, none, cu_k).shape == (0, 128)
+
+
+def test_cross_binding_refuses_wrong_operands():
+    q, k, v, cq, ck = _dev(*_data([5], [9], 4, 2, "bf16", 41))
+    for bad in (lambda: sra.cross_attention(q.cpu(), k, v, cq, ck), lambda: sra.cross_attention(q.float(), k, v, cq, ck),
+                lambda: sra.cross_attention(q, k.half(), v, cq, ck), lambda: sra.cross_attention(q, k, v[:8], cq, ck),
+                lambda: sra.cross_attention(q[:, :100], k, v, cq, ck), lambda: sra.cross_attention(q[:, :192], k, v, cq, ck),
+                lambda: sra.cross_attention(q, k, v, cq.long(), ck), lambda: sra.cross_attention(q, k, v, cq, ck[:1]),
+                lambda: sra.cross_attention(q, k, v, cq, ck, out=q.half()), lambda: sra.cross_attention(q.t(), k, v, cq, ck),
+                lambda: sra.cross_attention_weights(q, k, cq, ck, heads=torch.zeros(2, device="cuda")),
+                lambda: sra.cross_attention_weights(q, k, cq, ck, out=torch.zeros(4, 5, 8, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(sra.AsrError):
+        sra.cross_attention(q[:, 4:][:, :64], k[:, :64], v[:, :64], cq, ck)  # rows that do not start on 16 bytes
+
+
+def test_encoder_rows_to_decoder_reads():
+    """The operators in a row, as a decoder uses them: fp32 encoder rows quantised, one fp8 product for the keys
+    and values of three layers, the last layer's columns read by the attention, and its weights.  Each step is
+    held to the oracle on the step's own inputs."""
+    rng = np.random.default_rng(50)
+    d, layers, lq, lk = 256, 3, [4, 90], [390, 211]
+    x = rng.normal(size=(sum(lk), d)).astype(np.float32)
+    w = (rng.normal(size=(layers * 2 * d, d)) * 0.06).astype(np.float32)
+    b = rng.normal(size=layers * 2 * d).astype(np.float32) * 0.1
+    xc, xs = sra.quantize_fp8(torch.from_numpy(x).cuda())
+    wc, wsc = sra.quantize_fp8(torch.from_numpy(w).cuda(), 128)
+    kv = sra.linear_fp8(xc, xs, wc, wsc, torch.from_numpy(b).cuda())
+    ref = oracle.linear_fp8(*oracle.quantize_fp8(x), *oracle.quantize_fp8(w, 128), b)
+    err = np.abs(kv.double().cpu().numpy() - ref)
+    # d fp32 additions at 2^-23 of the magnitudes' sum (|x| |w| <= 2^8 here), half a bf16 step
+    assert (err <= d * 2.0 ** -23 * 256 + 2.0 ** -8 * np.abs(ref)).all()
+    at = (layers - 1) * 2 * d
+    k, v = kv[:, at:at + d], kv[:, at + d:]
+    q = torch.from_numpy(rng.normal(size=(sum(lq), d)).astype(np.float32) * 2).to(torch.bfloat16)
+    cu = lambda l: np.concatenate([[0], np.cumsum(l)]).astype(np.int32)  # noqa: E731
+    cu_q, cu_k = cu(lq), cu(lk)
+    cq, ck = torch.from_numpy(cu_q).cuda(), torch.from_numpy(cu_k).cuda()
+    out = sra.cross_attention(q.cuda(), k, v, cq, ck)
+    check_attention(out, q, k.cpu(), v.cpu(), cu_q, cu_k, "bf16")
+    weights = sra.cross_attention_weights(q.cuda(), k, cq, ck).double().cpu().numpy()
+    wref = oracle.cross_attention_weights(q.double().numpy(), k.double().cpu().numpy(), cu_q, cu_k, range(4), max(lk))
+    np.testing.assert_allclose(weights, wref, rtol=2e-4, atol=2.0 ** -126)
