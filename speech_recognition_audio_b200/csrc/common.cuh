@@ -91,26 +91,13 @@ static __device__ __noinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t pa
 
 // The same wait inline: a call's register saves cost a single-warp issuer
 // about 350 cycles a wait, completed barriers included.
-// CLUSTER: acquires what threads of other blocks of the cluster released.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t addr, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(addr), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, int* status, int code) {
   const uint32_t a = smem_u32(bar);
-  auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity); };
-  if (done()) return true;
+  if (mbar_try_wait(a, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
 #pragma unroll 1
   for (uint32_t it = 1;; ++it) {
-    if (done()) return true;
+    if (mbar_try_wait(a, parity)) return true;
     if (it % 32) continue;
     if (globaltimer_ns() - t0 > limit_ns) {
       if (status) atomicCAS(status, 0, code);
