@@ -496,11 +496,13 @@ def _raw_stream(stream, dev):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _rows(what, t, cols=None):
-    """Refuse anything but a 2-D tensor of contiguous elements within each row; returns its row stride."""
-    if t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1 or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{what}: need a 2-D tensor with contiguous rows" + (f" of {cols}" if cols is not None else ""))
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _rows(what, t):
+    """(rows, columns, row stride) of a 2-D tensor; refuses any whose rows are not contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{what}: need 2-D tensors with contiguous rows")
+    m, n = shape
+    return m, n, (stride[0] if m > 1 else max(stride[0], n))
 
 
 def _new(stream, shape, dtype, like, zero=False):
@@ -520,11 +522,10 @@ def quantize_fp8(x, block_rows: int = 1, stream=None):
     (1 or 128) x 128 (asr_op_quantize_fp8)."""
     torch = _t()
     dev = _operands("quantize_fp8", x)
-    ldx = _rows("quantize_fp8", x)
+    M, K, ldx = _rows("quantize_fp8", x)
     code = 0 if x.dtype is torch.bfloat16 else 1 if x.dtype is torch.float32 else 2 if x.dtype is torch.float16 else None
     if code is None:
         raise ValueError(f"quantize_fp8: {x.dtype} is not bf16, f16 or f32")
-    M, K = x.shape
     codes = _new(stream, (M, K), torch.float8_e4m3fn, x)
     scales = _new(stream, (-(-M // max(block_rows, 1)), -(-K // 128)), torch.float8_e8m0fnu, x)
     _check(lib.asr_op_quantize_fp8(x.data_ptr(), code, ldx, M, K, block_rows, codes.data_ptr(), scales.data_ptr(),
@@ -570,26 +571,28 @@ def linear_fp8(x, x_scales, w, w_scales, bias=None, epi: int = EPI_BF16, out=Non
 
 
 def _cross_operands(what, q, k, v, cu_q, cu_k, max_q, max_k, out, workspace):
-    """What the two cross-attention calls check alike -> (device, n_seg, max_q, max_k, H, Hkv, ldq, ldk, ldv)."""
+    """What the two cross-attention calls check alike -> (device, n_seg, max_q, max_k, Tq, Tk, H, Hkv, ldq,
+    ldk, ldv)."""
     torch = _t()
     dev = _operands(what, q, k, v, cu_q, cu_k, out, workspace)
     dt = q.dtype
     if (dt is not torch.bfloat16 and dt is not torch.float16) or k.dtype is not dt or (v is not None and v.dtype is not dt):
         raise ValueError(f"{what}: q, k and v must be of one type, bf16 or f16")
-    ldq, ldk = _rows(what, q), _rows(what, k)
-    wq, wk = q.shape[1], k.shape[1]
-    ldv = 0 if v is None else _rows(what, v, wk)
-    if not wq or not wk or wq % 64 or wk % 64 or wq % wk or (v is not None and v.shape[0] != k.shape[0]):
+    Tq, wq, ldq = _rows(what, q)
+    Tk, wk, ldk = _rows(what, k)
+    Tv, wv, ldv = (Tk, wk, 0) if v is None else _rows(what, v)
+    if not wq or not wk or wq % 64 or wk % 64 or wq % wk or Tv != Tk or wv != wk:
         raise ValueError(f"{what}: need q [Tq, H * 64] and k, v [Tk, Hkv * 64] with H a multiple of Hkv")
-    n_seg = cu_q.numel() - 1
-    if (cu_q.dtype is not torch.int32 or cu_k.dtype is not torch.int32 or cu_q.dim() != 1 or cu_q.shape != cu_k.shape
-            or n_seg < 1 or not cu_q.is_contiguous() or not cu_k.is_contiguous()):
+    seg = cu_q.shape
+    n_seg = seg[0] - 1 if len(seg) == 1 else 0
+    if (cu_q.dtype is not torch.int32 or cu_k.dtype is not torch.int32 or seg != cu_k.shape or n_seg < 1
+            or not cu_q.is_contiguous() or not cu_k.is_contiguous()):
         raise ValueError(f"{what}: cu_q and cu_k must be contiguous int32 [n_seg + 1]")
     if max_q is None:
         max_q = int((cu_q[1:] - cu_q[:-1]).max())
     if max_k is None:
         max_k = int((cu_k[1:] - cu_k[:-1]).max())
-    return dev, n_seg, max_q, max_k, wq // 64, wk // 64, ldq, ldk, ldv
+    return dev, n_seg, max_q, max_k, Tq, Tk, wq // 64, wk // 64, ldq, ldk, ldv
 
 
 def cross_attention(q, k, v, cu_q, cu_k, max_q=None, max_k=None, out=None, workspace=None, stream=None,
@@ -600,18 +603,19 @@ def cross_attention(q, k, v, cu_q, cu_k, max_q=None, max_k=None, out=None, works
     written (out keeps what it held).  workspace: a zeroed CUDA tensor of asr_op_cross_attention_ws_size()
     bytes; with check the call synchronises and raises on bad offsets."""
     torch = _t()
-    dev, n_seg, max_q, max_k, H, Hkv, ldq, ldk, ldv = _cross_operands("cross_attention", q, k, v, cu_q, cu_k, max_q,
-                                                                      max_k, out, workspace)
+    dev, n_seg, max_q, max_k, Tq, Tk, H, Hkv, ldq, ldk, ldv = _cross_operands("cross_attention", q, k, v, cu_q, cu_k,
+                                                                              max_q, max_k, out, workspace)
     if out is None:
-        out = _new(stream, q.shape, q.dtype, q)
+        out, ldo = _new(stream, (Tq, 64 * H), q.dtype, q), 64 * H
     elif out.dtype is not q.dtype or out.shape != q.shape:
         raise ValueError("cross_attention: out must be like q")
-    ldo = _rows("cross_attention", out)
+    else:
+        ldo = _rows("cross_attention", out)[2]
     if workspace is None:
         workspace = _new(stream, (256,), torch.uint8, q, zero=True)
     st = _raw_stream(stream, dev)
     _check(lib.asr_op_cross_attention(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, cu_q.data_ptr(),
-                                      cu_k.data_ptr(), n_seg, max_q, max_k, q.shape[0], k.shape[0], H, Hkv,
+                                      cu_k.data_ptr(), n_seg, max_q, max_k, Tq, Tk, H, Hkv,
                                       2 if q.dtype is torch.float16 else 0, out.data_ptr(), ldo, workspace.data_ptr(),
                                       workspace.nbytes, st))
     if check:
@@ -627,9 +631,8 @@ def cross_attention_weights(q, k, cu_q, cu_k, max_q=None, max_k=None, heads=None
     32 bytes."""
     torch = _t()
     what = "cross_attention_weights"
-    dev, n_seg, max_q, max_k, H, Hkv, ldq, ldk, _ = _cross_operands(what, q, k, None, cu_q, cu_k, max_q, max_k, out,
-                                                                    workspace)
-    Tq = q.shape[0]
+    dev, n_seg, max_q, max_k, Tq, Tk, H, Hkv, ldq, ldk, _ = _cross_operands(what, q, k, None, cu_q, cu_k, max_q, max_k,
+                                                                            out, workspace)
     if heads is None:
         n, hp = H, None
     elif heads.get_device() != dev or heads.dtype is not torch.int32 or heads.dim() != 1 or not heads.is_contiguous():
@@ -650,7 +653,7 @@ def cross_attention_weights(q, k, cu_q, cu_k, max_q=None, max_k=None, heads=None
         workspace = _new(stream, (256,), torch.uint8, q, zero=True)
     st = _raw_stream(stream, dev)
     _check(lib.asr_op_cross_attention_weights(q.data_ptr(), ldq, k.data_ptr(), ldk, cu_q.data_ptr(), cu_k.data_ptr(),
-                                              n_seg, max_q, max_k, Tq, k.shape[0], H, Hkv,
+                                              n_seg, max_q, max_k, Tq, Tk, H, Hkv,
                                               2 if q.dtype is torch.float16 else 0, hp, n, out.data_ptr(),
                                               ldw, workspace.data_ptr(), workspace.nbytes, st))
     if check:
