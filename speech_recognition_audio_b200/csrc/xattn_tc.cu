@@ -21,7 +21,8 @@
 // MHz): 605 us.  Measured on the way there: single-lane issue with waits behind
 // a call 868; one thread a row and two tiles a block 617, with the tiles'
 // exponentials taking turns 762; exponentials ahead of the maximum, repeated
-// where it moved, 615.
+// where it moved, 615; two independent streams of 64-state tiles a block, P over
+// S, 626.
 //
 // The running maximum used for the exponentials moves only when a row's
 // maximum exceeds it by more than 2^8 (then O and the sum are rescaled), so
