@@ -11,18 +11,18 @@
 //             the next tile's product runs under the exponentials.
 // Tensor memory: S 128, P 64, O 64 columns, none shared.
 //
-// What bounds it is the softmax: 16 exponentials per clock and SM against 4096
-// products, so a tile of 128 x 128 costs 1024 clocks of them and 512 of the
-// tensor pipe, and a warp's own chain (wait, read, maximum, exponentials,
-// write) is about twice as long as its exponentials.  Four softmax warps per
-// scheduler keep that unit about half busy; the two warps a block puts on a
-// scheduler move in step, which is why it is not more.  2240 rows x 1500 states
-// x 12 heads x 32 segments (330 GFLOP, 1.29e9 exponentials = 277 us at 1965
-// MHz): 605 us.  Measured on the way there: single-lane issue with waits behind
-// a call 868; one thread a row and two tiles a block 617, with the tiles'
-// exponentials taking turns 762; exponentials ahead of the maximum, repeated
-// where it moved, 615; two independent streams of 64-state tiles a block, P over
-// S, 626.
+// Floors: 16 exponentials per clock and SM against 4096 products, so a tile of
+// 128 x 128 costs 1024 clocks of them and 512 of the tensor pipe.  2240 rows x
+// 1500 states x 12 heads x 32 segments (330 GFLOP, 1.29e9 exponentials = 277 us
+// at 1965 MHz): 602 us.  What bounds it is the chain of a step (wait, read,
+// maximum, exponentials, write, product), of which four softmax warps per
+// scheduler hide about half: without the exponentials it takes 479 us, without
+// them and the maxima 443.  Measured on the way there: single-lane issue with
+// waits behind a call 868; one thread a row and two tiles a block 617, with
+// the tiles' exponentials taking turns 762; exponentials ahead of the maximum,
+// repeated where it moved, 615; two independent streams of 64-state tiles a
+// block, P over S, 626; persistent blocks running ahead into the next tile of
+// rows, with two K tiles in flight, 681.
 //
 // The running maximum used for the exponentials moves only when a row's
 // maximum exceeds it by more than 2^8 (then O and the sum are rescaled), so
