@@ -3,7 +3,8 @@
  *
  * Each call runs one stage of the forward pass with exactly the kernel that
  * asr_enc_forward launches for it, on caller-owned device buffers, so that
- * every stage can be checked on its own.  Conventions as in asr_enc.h
+ * every stage can be checked on its own; the fp8 and cross-attention calls
+ * serve a decoder that reads the encoder's output.  Conventions as in asr_enc.h
  * (device pointers, stream as void*, asr_status return, asynchronous).
  */
 #ifndef ASR_OPS_H
