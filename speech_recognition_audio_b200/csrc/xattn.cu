@@ -437,15 +437,23 @@ __global__ void __launch_bounds__(32 * XW_WARPS, 2) xattn_weights_kernel(const X
 // (warps x blocks) at 1500 keys unless stated: 12 tiles 4x1 11.5, 4x8 5.4,
 // 16x8 5.5; 24 tiles 4x8 6.5, 16x4 6.0; 96 tiles 4x1 18.4, 4x4 12.4, 16x1 11.9,
 // 16x4 19.3; 192 tiles 4x1 21.6, 8x1 17.6, 16x1 22.9; 384 tiles (5 rows) 4x1
-// 30.2, 8x1 34.3, 4x2 36.5; 16 tiles at up to 30000 keys 4x8 41.0, 16x8 22.2.
+// 30.2, 8x1 34.3, 4x2 36.5; 16 tiles at up to 30000 keys 4x8 41.0, 16x8 22.2; 4
+// tiles at 30000 keys 16x8 19.3, 16x16 12.7.
 template <int KIND, int NB>
 static cudaError_t launch_rows(XattnArgs a, int n_seg, int max_k, int num_sms, cudaStream_t st) {
   const int tiles = (int)(((long long)a.max_q * a.G + 8 * NB - 1) / (8 * NB)), Hkv = a.H / a.G;
   const long long blocks = (long long)n_seg * tiles * Hkv, want = 10LL * num_sms;
   int W = 4;
   while (W < (NB == 1 ? 16 : 8) && blocks * W < want) W *= 2;
-  a.splits = pick_splits(blocks * W, max_k, 8 * W, want);
+  a.splits = pick_splits(blocks * W, max_k, 8 * W, want, W == 4 ? 8 : 16);
   const dim3 grid(n_seg * a.splits, tiles, Hkv);
+  if (a.splits > 8) {
+    static std::atomic<unsigned long long> wide[2] = {{0}, {0}};
+    cudaError_t r = allow_wide_clusters(xattn_rows_kernel<KIND, NB, 8>, wide[0]);
+    if constexpr (NB == 1)
+      if (r == cudaSuccess) r = allow_wide_clusters(xattn_rows_kernel<KIND, NB, 16>, wide[1]);
+    if (r != cudaSuccess) return r;
+  }
   if (W == 4) return launch_cluster(xattn_rows_kernel<KIND, NB, 4>, grid, 128, 0, a.splits, st, a);
   if (W == 8) return launch_cluster(xattn_rows_kernel<KIND, NB, 8>, grid, 256, 0, a.splits, st, a);
   if constexpr (NB == 1) return launch_cluster(xattn_rows_kernel<KIND, NB, 16>, grid, 512, 0, a.splits, st, a);

@@ -47,13 +47,24 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 // exp(-inf - m) is 0 there and not NaN.
 __device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.f : m; }
 
-// Blocks a (segment, tile, head) is split into: a power of two up to the
-// portable cluster size, while the grid does not yet fill `fill` blocks and
-// each block keeps at least `least` keys.
-inline int pick_splits(long long blocks, int keys, int least, long long fill) {
+// Blocks a (segment, tile, head) is split into: a power of two, as long as the
+// grid does not yet fill `fill` blocks and each block keeps at least `least`
+// keys; up to `most` (8 is the portable cluster size, 16 needs allow_wide_clusters).
+inline int pick_splits(long long blocks, int keys, int least, long long fill, int most = 8) {
   int s = 1;
-  while (s < 8 && blocks * s < fill && keys >= 2 * s * least) s *= 2;
+  while (s < most && blocks * s < fill && keys >= 2 * s * least) s *= 2;
   return s;
+}
+// Lets a kernel be launched in clusters of 16, once per device.
+template <typename... KArgs>
+cudaError_t allow_wide_clusters(void (*kernel)(KArgs...), std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) & bit))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace asr

@@ -367,6 +367,11 @@ static cudaError_t launch_tiles(const CUtensorMap& q, const CUtensorMap& k, cons
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = set_smem_once(kern, XT_SMEM, done);
   if (e != cudaSuccess) return e;
+  if (a.splits > 8) {
+    static std::atomic<unsigned long long> wide{0};
+    const cudaError_t r = allow_wide_clusters(kern, wide);
+    if (r != cudaSuccess) return r;
+  }
   const int q_blocks = (a.max_q + 127) / 128;
   return launch_cluster(kern, dim3(n_seg * q_blocks * a.splits, a.H), XT_THREADS, XT_SMEM, a.splits, st, q, k, v, a, q_blocks);
 }
@@ -377,7 +382,16 @@ cudaError_t launch_xattn_tiles(XattnArgs a, int n_seg, int max_k, bool f16, int 
       !make_tmap_bf16(&k, a.k, a.Tk, 64ULL * (a.H / a.G), a.ldk, 128) ||
       !make_tmap_bf16(&v, a.v, a.Tk, 64ULL * (a.H / a.G), a.ldv, 128))
     return cudaErrorInvalidValue;
-  a.splits = pick_splits((long long)n_seg * ((a.max_q + 127) / 128) * a.H, max_k, 256, 2 * num_sms);
+  // Splits S: a tile of states takes about 1.5 us, and each block of a cluster
+  // costs about 0.12 us to get going, so the S with the least
+  // 12.5 tiles / S + blocks S.  Measured, us, at 1, 8 and 16 (or the most that
+  // leaves a block a tile): 4 blocks x 235 tiles 281, 48, 33; 12 x 235 282, 51,
+  // 47; 12 x 63 80, 23, 25; 12 x 12 19, 14; 48 x 12 20, 22; 96 x 12 20, 33.
+  const double blocks = (double)n_seg * ((a.max_q + 127) / 128) * a.H, tiles = (max_k + 127) / 128;
+  double least = 12.5 * tiles;
+  a.splits = 1;
+  for (int S = 2; S <= 16 && S <= tiles && blocks * S <= 2 * num_sms; S *= 2)
+    if (12.5 * tiles / S + blocks * S < least) a.splits = S, least = 12.5 * tiles / S + blocks * S;
   return f16 ? launch_tiles<KIND_F16>(q, k, v, a, n_seg, st) : launch_tiles<KIND_BF16>(q, k, v, a, n_seg, st);
 }
 
