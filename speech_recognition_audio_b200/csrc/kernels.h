@@ -191,7 +191,8 @@ struct XattnArgs {
 };
 cudaError_t launch_xattn(XattnArgs a, int n_seg, int max_k, bool f16, int num_sms, cudaStream_t st);
 cudaError_t launch_xattn_tiles(XattnArgs a, int n_seg, int max_k, bool f16, int num_sms, cudaStream_t st);  // xattn_tc.cu
-cudaError_t launch_xattn_weights_tiles(XattnArgs a, int n_seg, int n_sel, bool f16, cudaStream_t st);  // xattn_tc.cu
+cudaError_t launch_xattn_weights_tiles(XattnArgs a, int n_seg, int n_sel, bool f16, int num_sms,
+                                       cudaStream_t st);  // xattn_tc.cu
 cudaError_t launch_xattn_weights(XattnArgs a, int n_seg, int n_sel, bool f16, int num_sms, cudaStream_t st);
 
 // fp8 with block scales (fp8.cu).  x_dtype: SPLICE_*; block_rows 1 or 128.

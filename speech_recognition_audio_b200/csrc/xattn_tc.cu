@@ -376,22 +376,27 @@ static cudaError_t launch_tiles(const CUtensorMap& q, const CUtensorMap& k, cons
   return launch_cluster(kern, dim3(n_seg * q_blocks * a.splits, a.H), XT_THREADS, XT_SMEM, a.splits, st, q, k, v, a, q_blocks);
 }
 
+// Splits S: a tile of states takes about 1.5 us a pass, and each block of a
+// cluster costs about 0.12 us to get going, so the S with the least
+// cost tiles / S + blocks S, cost = 12.5 a pass.  Measured (attention, us) at 1,
+// 8 and 16, or the most that leaves a block a tile: 4 blocks x 235 tiles 281,
+// 48, 33; 12 x 235 282, 51, 47; 12 x 63 80, 23, 25; 12 x 12 19, 14; 48 x 12 20,
+// 22; 96 x 12 20, 33.
+static int xt_splits(double blocks, int tiles, double cost, int num_sms) {
+  double least = cost * tiles;
+  int best = 1;
+  for (int S = 2; S <= 16 && S <= tiles && blocks * S <= 2 * num_sms; S *= 2)
+    if (cost * tiles / S + blocks * S < least) best = S, least = cost * tiles / S + blocks * S;
+  return best;
+}
+
 cudaError_t launch_xattn_tiles(XattnArgs a, int n_seg, int max_k, bool f16, int num_sms, cudaStream_t st) {
   CUtensorMap q, k, v;
   if (!make_tmap_bf16(&q, a.q, a.Tq, 64ULL * a.H, a.ldq, 128) ||
       !make_tmap_bf16(&k, a.k, a.Tk, 64ULL * (a.H / a.G), a.ldk, 128) ||
       !make_tmap_bf16(&v, a.v, a.Tk, 64ULL * (a.H / a.G), a.ldv, 128))
     return cudaErrorInvalidValue;
-  // Splits S: a tile of states takes about 1.5 us, and each block of a cluster
-  // costs about 0.12 us to get going, so the S with the least
-  // 12.5 tiles / S + blocks S.  Measured, us, at 1, 8 and 16 (or the most that
-  // leaves a block a tile): 4 blocks x 235 tiles 281, 48, 33; 12 x 235 282, 51,
-  // 47; 12 x 63 80, 23, 25; 12 x 12 19, 14; 48 x 12 20, 22; 96 x 12 20, 33.
-  const double blocks = (double)n_seg * ((a.max_q + 127) / 128) * a.H, tiles = (max_k + 127) / 128;
-  double least = 12.5 * tiles;
-  a.splits = 1;
-  for (int S = 2; S <= 16 && S <= tiles && blocks * S <= 2 * num_sms; S *= 2)
-    if (12.5 * tiles / S + blocks * S < least) a.splits = S, least = 12.5 * tiles / S + blocks * S;
+  a.splits = xt_splits((double)n_seg * ((a.max_q + 127) / 128) * a.H, (max_k + 127) / 128, 12.5, num_sms);
   return f16 ? launch_tiles<KIND_F16>(q, k, v, a, n_seg, st) : launch_tiles<KIND_BF16>(q, k, v, a, n_seg, st);
 }
 
@@ -439,13 +444,20 @@ __global__ void __launch_bounds__(320, 2)
   pdl_wait();
   pdl_trigger();
 
-  const int seg = blockIdx.x / q_blocks, row0 = (blockIdx.x - seg * q_blocks) * 128, sel = blockIdx.y;
+  const int S = a.splits, rank = blockIdx.x % S, unit = blockIdx.x / S;
+  const int seg = unit / q_blocks, row0 = (unit - seg * q_blocks) * 128, sel = blockIdx.y;
   const Segment s = load_segment(a, seg, tid == 0);
   const int h = a.heads ? __ldg(a.heads + sel) : sel;
   const bool head_ok = h >= 0 && h < a.H;
   if (!head_ok && tid == 0) atomicCAS(a.status, 0, DEV_BAD_SEGMENT);
-  const bool live = s.ok && head_ok && row0 < s.lq;
-  const int nk = (s.lk + 127) / 128;
+  const bool live = s.ok && head_ok && row0 < s.lq;  // the same for every block of the cluster
+  // this block's tiles of columns, and how many of them hold states
+  const int tiles = (a.width + 127) / 128;
+  const int t0 = (int)((long long)rank * tiles / S), t1 = (int)((long long)(rank + 1) * tiles / S);
+  const int nk = max(0, min(t1, (s.lk + 127) / 128) - t0);
+  // Cluster barriers: the load and issue warps arrive at the first at once (it
+  // only guards the softmax warps' statistics) and wait at their end.
+  if (S > 1 && live && warp >= XT_TMA_WARP) cluster_arrive();
 
   if (live && nk > 0 && warp == XT_TMA_WARP) {
     if (lane == 0) {
@@ -453,7 +465,7 @@ __global__ void __launch_bounds__(320, 2)
       tma_load_2d(sm, &tm_q, &bar[WB_Q], h * 64, s.q0 + row0);
       int n = 0;
       for (; n < 2 * nk; ++n) {
-        const int ks = n % XWT_KS, j = n < nk ? n : n - nk;
+        const int ks = n % XWT_KS, j = t0 + (n < nk ? n : n - nk);
         if (!mbar_wait(&bar[WB_KE + ks], ((n / XWT_KS) & 1) ^ 1, a.limit_ns, &failed, DEV_TIMEOUT_PRODUCER)) break;
         mbar_arrive_expect_tx(&bar[WB_KF + ks], XT_TILE);
         tma_load_2d(sm + XWT_SK + ks * XT_TILE, &tm_k, &bar[WB_KF + ks], h / a.G * 64, s.k0 + j * 128);
@@ -498,10 +510,10 @@ __global__ void __launch_bounds__(320, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[WB_SE + (n & 1)]);
     };
-    for (int j = 0; j < nk; ++j) {
+    for (int n = 0; n < nk; ++n) {
       float v[64];
-      scores(j, v);
-      const int kv = s.lk - j * 128 - 64 * hh;  // states of this half
+      scores(n, v);
+      const int kv = s.lk - (t0 + n) * 128 - 64 * hh;  // states of this half
       if (kv < 64) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
@@ -526,22 +538,38 @@ __global__ void __launch_bounds__(320, 2)
       }
       l += ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y));
     }
-    if (nk > 0) {
-      float2* red = reinterpret_cast<float2*>(sm + XWT_RED);
-      red[hh * 128 + row] = make_float2(m, l);
+    // the row's maximum and sum: over both halves, and over the cluster's
+    // blocks in rank order
+    float2* red = reinterpret_cast<float2*>(sm + XWT_RED);
+    red[hh * 128 + row] = make_float2(m, l);
+    if (S > 1)
+      cluster_sync();
+    else
       pair_sync(q);
-      const float2 x = red[row], y = red[128 + row];
-      sh = shift_of(fmaxf(x.x, y.x));
-      inv = 1.0f / (x.y * ex2_approx(x.x - sh) + y.y * ex2_approx(y.x - sh));
+    if (s.lk > 0) {
+      const uint32_t mine = smem_u32(&red[row]);
+      float mm = -INFINITY, ll = 0.f;
+      for (int i = 0; i < 2 * S; ++i) {
+        const uint32_t p = mapa_shared(mine, S > 1 ? i >> 1 : 0) + (i & 1) * (128 * 8);
+        mm = fmaxf(mm, S > 1 ? ld_cluster_f32(p) : red[(i & 1) * 128 + row].x);
+      }
+      sh = shift_of(mm);
+      for (int i = 0; i < 2 * S; ++i) {
+        const uint32_t p = mapa_shared(mine, S > 1 ? i >> 1 : 0) + (i & 1) * (128 * 8);
+        const float2 x = S > 1 ? make_float2(ld_cluster_f32(p), ld_cluster_f32(p + 4)) : red[(i & 1) * 128 + row];
+        ll = fmaf(x.y, ex2_approx(x.x - sh), ll);
+      }
+      inv = 1.0f / ll;
     }
+    if (S > 1) cluster_arrive();  // the others' statistics have been read
     uint8_t* buf = sm + XWT_BUF + warp * 4096;
     const int rows = s.lq - row0 - 32 * q;  // valid rows of this warp, if fewer than 32
     const long long orow = (long long)sel * a.Tq + s.q0 + row0 + 32 * q;
     const bool vec = ((reinterpret_cast<uintptr_t>(a.out) & 15) | (a.ldo & 3)) == 0;
-    for (int j = 0; j * 128 + 64 * hh < a.width && rows > 0; ++j) {
+    for (int j = t0; j < t1 && j * 128 + 64 * hh < a.width && rows > 0; ++j) {
       float v[64];
-      if (j < nk) {
-        scores(nk + j, v);
+      if (j - t0 < nk) {
+        scores(nk + j - t0, v);
       } else {
 #pragma unroll
         for (int c = 0; c < 64; ++c) v[c] = 0.f;  // columns past the states: zeros below
@@ -605,13 +633,21 @@ __global__ void __launch_bounds__(320, 2)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[WB_SE + ((nk + j) & 1)]);
       }
-    } else if (nk > 0 && (nk - 1) * 128 + 64 * hh >= a.width) {
+    } else if (nk > 0 && (t0 + nk - 1) * 128 + 64 * hh >= a.width) {
       // (the last tile's second half lies past the width)
       ok = ok && mbar_wait(&bar[WB_SF + ((2 * nk - 1) & 1)], ((2 * nk - 1) >> 1) & 1, a.limit_ns, &failed, DEV_TIMEOUT_EPILOGUE);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[WB_SE + ((2 * nk - 1) & 1)]);
     }
     if (lane == 0) bulk_wait0();
+    __syncwarp();
+    if (S > 1) cluster_wait();  // no block leaves while another may read its statistics
+  }
+  if (S > 1 && live && warp >= XT_TMA_WARP) {
+    __syncwarp();
+    cluster_wait();
+    cluster_arrive();
+    cluster_wait();
   }
   tc_fence_before();
   __syncthreads();
@@ -620,7 +656,7 @@ __global__ void __launch_bounds__(320, 2)
   if (tid == 0 && failed) atomicCAS(a.status, 0, failed);
 }
 
-cudaError_t launch_xattn_weights_tiles(XattnArgs a, int n_seg, int n_sel, bool f16, cudaStream_t st) {
+cudaError_t launch_xattn_weights_tiles(XattnArgs a, int n_seg, int n_sel, bool f16, int num_sms, cudaStream_t st) {
   CUtensorMap q, k, o;
   if (!make_tmap_bf16(&q, a.q, a.Tq, 64ULL * a.H, a.ldq, 128) ||
       !make_tmap_bf16(&k, a.k, a.Tk, 64ULL * (a.H / a.G), a.ldk, 128))
@@ -628,11 +664,18 @@ cudaError_t launch_xattn_weights_tiles(XattnArgs a, int n_seg, int n_sel, bool f
   const bool tma = n_sel * a.Tq < (1LL << 31) && make_tmap_out(&o, a.out, n_sel * a.Tq, a.width, a.ldo, true);
   if (!tma) o = k;
   const int q_blocks = (a.max_q + 127) / 128;
+  // as for the attention, with two passes over each tile
+  a.splits = xt_splits((double)n_seg * q_blocks * n_sel, (a.width + 127) / 128, 25.0, num_sms);
   auto kern = f16 ? xattn_weights_tiles_kernel<KIND_F16> : xattn_weights_tiles_kernel<KIND_BF16>;
   static std::atomic<unsigned long long> done[2] = {{0}, {0}};
   const cudaError_t e = set_smem_once(kern, XWT_SMEM, done[f16]);
   if (e != cudaSuccess) return e;
-  return launch_cluster(kern, dim3(n_seg * q_blocks, n_sel), 320, XWT_SMEM, 1, st, q, k, o, a, q_blocks, (int)tma);
+  if (a.splits > 8) {
+    static std::atomic<unsigned long long> wide[2] = {{0}, {0}};
+    const cudaError_t r = allow_wide_clusters(kern, wide[f16]);
+    if (r != cudaSuccess) return r;
+  }
+  return launch_cluster(kern, dim3(n_seg * q_blocks * a.splits, n_sel), 320, XWT_SMEM, a.splits, st, q, k, o, a, q_blocks, (int)tma);
 }
 
 }  // namespace asr

@@ -24,6 +24,7 @@ LENGTHS = {
     "prompt": ([224, 100], [1500, 390]),
     "rows": ([300, 1, 129], [257, 128, 1]),
     "long": ([2], [30001]),
+    "deep": ([40], [20011]),
 }
 
 
@@ -163,7 +164,7 @@ def test_peaked_rows_and_rising_maxima(lq):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("case", ["one", "step", "beams", "empty", "tiles", "prompt", "rows", "long"])
+@pytest.mark.parametrize("case", ["one", "step", "beams", "empty", "tiles", "prompt", "rows", "long", "deep"])
 @pytest.mark.parametrize("H,Hkv,heads", [(4, 4, None), (6, 2, [5, 0, 3])])
 def test_cross_attention_weights(case, H, Hkv, heads, dtype):
     lq, lk = LENGTHS[case]
