@@ -21,6 +21,7 @@ The entry points mirror ``include/asr_enc.h`` and ``include/asr_ops.h``:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -505,6 +506,14 @@ def _rows(what, t):
     return m, n, (stride[0] if m > 1 else max(stride[0], n))
 
 
+def _on(stream):
+    """The context in which torch's own work goes to `stream`: nothing to change for None."""
+    if stream is None:
+        return contextlib.nullcontext()
+    torch = _t()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 def _new(stream, shape, dtype, like, zero=False):
     """A tensor allocated for `stream`, so that what a call allocates and drops is not handed out again
     before that stream is done with it."""
@@ -514,7 +523,7 @@ def _new(stream, shape, dtype, like, zero=False):
         if len(shape) == 2 and not zero:  # the same tensor, two thirds of empty()'s time
             return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=like.device)
         return make(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+    with _on(stream):
         return make(shape, dtype=dtype, device=like.device)
 
 
@@ -572,7 +581,13 @@ def linear_fp8(x, x_scales, w, w_scales, bias=None, epi: int = EPI_BF16, out=Non
     return out
 
 
-def _cross_operands(what, q, k, v, cu_q, cu_k, max_q, max_k, out, workspace):
+def _longest(cu, stream):
+    """The longest segment, from the offsets as `stream` leaves them."""
+    with _on(stream):
+        return int((cu[1:] - cu[:-1]).max())
+
+
+def _cross_operands(what, q, k, v, cu_q, cu_k, max_q, max_k, out, workspace, stream):
     """What the two cross-attention calls check alike -> (device, n_seg, max_q, max_k, Tq, Tk, H, Hkv, ldq,
     ldk, ldv)."""
     torch = _t()
@@ -591,9 +606,9 @@ def _cross_operands(what, q, k, v, cu_q, cu_k, max_q, max_k, out, workspace):
             or not cu_q.is_contiguous() or not cu_k.is_contiguous()):
         raise ValueError(f"{what}: cu_q and cu_k must be contiguous int32 [n_seg + 1]")
     if max_q is None:
-        max_q = int((cu_q[1:] - cu_q[:-1]).max())
+        max_q = _longest(cu_q, stream)
     if max_k is None:
-        max_k = int((cu_k[1:] - cu_k[:-1]).max())
+        max_k = _longest(cu_k, stream)
     return dev, n_seg, max_q, max_k, Tq, Tk, wq // 64, wk // 64, ldq, ldk, ldv
 
 
@@ -601,12 +616,12 @@ def cross_attention(q, k, v, cu_q, cu_k, max_q=None, max_k=None, out=None, works
                     check: bool = True):
     """q CUDA [Tq, H*64], k and v CUDA [Tk, Hkv*64] (bf16 or f16, rows may be strided: a layer's columns of a
     product over all layers), cu_q / cu_k int32 CUDA [n_seg+1] -> [Tq, H*64] (asr_op_cross_attention).  Without
-    max_q / max_k they are read from the device (a synchronisation).  Rows outside every segment are not
+    max_q / max_k they are read from the device, behind what `stream` holds (a synchronisation with it).  Rows outside every segment are not
     written (out keeps what it held).  workspace: a zeroed CUDA tensor of asr_op_cross_attention_ws_size()
     bytes; with check the call synchronises and raises on bad offsets."""
     torch = _t()
     dev, n_seg, max_q, max_k, Tq, Tk, H, Hkv, ldq, ldk, ldv = _cross_operands("cross_attention", q, k, v, cu_q, cu_k,
-                                                                              max_q, max_k, out, workspace)
+                                                                              max_q, max_k, out, workspace, stream)
     if out is None:
         out, ldo = _new(stream, (Tq, 64 * H), q.dtype, q), 64 * H
     elif out.dtype is not q.dtype or out.shape != q.shape:
@@ -634,7 +649,7 @@ def cross_attention_weights(q, k, cu_q, cu_k, max_q=None, max_k=None, heads=None
     torch = _t()
     what = "cross_attention_weights"
     dev, n_seg, max_q, max_k, Tq, Tk, H, Hkv, ldq, ldk, _ = _cross_operands(what, q, k, None, cu_q, cu_k, max_q, max_k,
-                                                                            out, workspace)
+                                                                            out, workspace, stream)
     if heads is None:
         n, hp = H, None
     elif heads.get_device() != dev or heads.dtype is not torch.int32 or heads.dim() != 1 or not heads.is_contiguous():
