@@ -451,14 +451,15 @@ def attention(qkv, cu, n_heads: int, stream=None):
     """qkv bf16 [T, 3*H*64], cu int32 CUDA [n_seg+1] -> bf16 [T, H*64]."""
     import torch
     T = qkv.shape[0]
-    cu_host = cu.cpu().tolist()
-    max_seg = max(b - a for a, b in zip(cu_host[:-1], cu_host[1:]))
-    out = torch.empty((T, n_heads * 64), dtype=torch.bfloat16, device=qkv.device)
-    ws = torch.zeros(int(lib.asr_op_attention_ws_size()), dtype=torch.uint8, device=qkv.device)
-    _check(lib.asr_op_attention(_ptr(qkv), _ptr(cu), len(cu_host) - 1, max_seg, T, n_heads, _ptr(out), _ptr(ws),
-                                ws.numel(), _stream(stream)))
-    if int(ws[:4].view(torch.int32).item()) != 0:
-        raise AsrError(6, "attention: a bounded device wait gave up")
+    with _on(stream):  # the offsets as `stream` leaves them, and the status word once its work is done
+        cu_host = cu.cpu().tolist()
+        max_seg = max(b - a for a, b in zip(cu_host[:-1], cu_host[1:]))
+        out = torch.empty((T, n_heads * 64), dtype=torch.bfloat16, device=qkv.device)
+        ws = torch.zeros(int(lib.asr_op_attention_ws_size()), dtype=torch.uint8, device=qkv.device)
+        _check(lib.asr_op_attention(_ptr(qkv), _ptr(cu), len(cu_host) - 1, max_seg, T, n_heads, _ptr(out), _ptr(ws),
+                                    ws.numel(), _stream(stream)))
+        if int(ws[:4].view(torch.int32).item()) != 0:
+            raise AsrError(6, "attention: a bounded device wait gave up")
     return out
 
 

@@ -55,3 +55,16 @@ def test_maxima_are_read_on_the_given_stream(handle, stale):
     w = sra.cross_attention_weights(q, k, lq, lk, stream=on)
     side.synchronize()
     assert w.shape == ref[1].shape and torch.equal(w, ref[1])
+
+
+@pytest.mark.parametrize("handle", list(HANDLES))
+@pytest.mark.parametrize("lengths", [[100, 60], [300, 4]])
+def test_self_attention_reads_its_segments_on_the_given_stream(handle, lengths):
+    torch.manual_seed(4)
+    qkv = torch.randn(sum(lengths), 3 * 128, device="cuda").bfloat16()
+    cu = _cu(lengths)
+    ref = sra.attention(qkv, cu, 2)
+    side = torch.cuda.Stream()
+    out = sra.attention(qkv, _late(side, cu, _cu([1, 2])), 2, stream=HANDLES[handle](side))
+    side.synchronize()
+    assert torch.equal(out, ref)
