@@ -185,7 +185,9 @@ asr_status asr_op_quantize_fp8(const void* x, int x_dtype, int64_t ldx, int64_t 
  *          int32 is the status word.  Zero it once before its first use: a
  *          call writes the word only when a bounded device wait gives up, and
  *          never clears it, so calls on one stream or several may share it
- *          and one look at the end covers them all.
+ *          and one look at the end covers them all: asr_op_linear_fp8_check()
+ *          synchronises the stream and turns the word into ASR_OK or
+ *          ASR_E_DEVICE_TIMEOUT.
  * Limits: M >= 1, K % 16 == 0, N % 16 == 0 (SwiGLU: N % 32 == 0), operands
  * 16-byte aligned.  A NaN code or scale makes the outputs of its row or
  * column NaN. */
@@ -194,6 +196,7 @@ size_t asr_op_linear_fp8_ws_size(void);
 asr_status asr_op_linear_fp8(const void* x, const void* xs, const void* w, const void* ws, const float* bias,
                              int64_t M, int N, int K, int epi, void* y, void* scratch, size_t scratch_bytes,
                              void* stream);
+asr_status asr_op_linear_fp8_check(const void* scratch, void* stream);
 
 /* ---- cross attention ---------------------------------------------------------
  * A decoder's tokens over the encoder states of their clip ("CrisperWhisper ->

@@ -108,6 +108,7 @@ def _load():
         "asr_op_quantize_fp8": (I, [P, I, I64, I64, I, I, P, P, P]),
         "asr_op_linear_fp8_ws_size": (SZ, []),
         "asr_op_linear_fp8": (I, [P, P, P, P, P, I64, I, I, I, P, P, SZ, P]),
+        "asr_op_linear_fp8_check": (I, [P, P]),
         "asr_op_cross_attention_ws_size": (SZ, []),
         "asr_op_cross_attention": (I, [P, I64, P, I64, P, I64, P, P, I, I, I, I64, I64, I, I, I, P, I64, P, SZ, P]),
         "asr_op_cross_attention_check": (I, [P, P]),
@@ -545,11 +546,14 @@ def quantize_fp8(x, block_rows: int = 1, stream=None):
     return codes, scales
 
 
-def linear_fp8(x, x_scales, w, w_scales, bias=None, epi: int = EPI_BF16, out=None, workspace=None, stream=None):
+def linear_fp8(x, x_scales, w, w_scales, bias=None, epi: int = EPI_BF16, out=None, workspace=None, stream=None,
+               check=None):
     """Quantised x [M, K] and w [N, K] (float8_e4m3fn codes, float8_e8m0fnu scales: quantize_fp8(x) and
     quantize_fp8(w, 128)), bias f32 [N] -> epilogue(x w^T + bias) (asr_op_linear_fp8).  workspace: a zeroed
     CUDA tensor of asr_op_linear_fp8_ws_size() bytes whose first int32 the call sets if a device wait gives up;
-    a program that calls this often keeps one."""
+    a program that calls this often keeps one and looks at it when it likes.  With check the call synchronises and
+    raises on such a wait; None: where the call makes the workspace itself (a call that is being captured into a
+    graph cannot, and leaves the word unread)."""
     torch = _t()
     dev = _operands("linear_fp8", x, x_scales, w, w_scales, bias, out, workspace)
     if x.dim() != 2 or w.dim() != 2:
@@ -576,9 +580,15 @@ def linear_fp8(x, x_scales, w, w_scales, bias=None, epi: int = EPI_BF16, out=Non
         raise ValueError(f"linear_fp8: out must be a contiguous {dt} tensor of shape {shape}")
     if workspace is None:
         workspace = _new(stream, (256,), torch.uint8, x, zero=True)
+        if check is None:
+            with _on(stream):
+                check = not torch.cuda.is_current_stream_capturing()
+    st = _raw_stream(stream, dev)
     _check(lib.asr_op_linear_fp8(x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
                                  None if bias is None else bias.data_ptr(), M, N, K, epi, out.data_ptr(),
-                                 workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev)))
+                                 workspace.data_ptr(), workspace.nbytes, st))
+    if check:
+        _check(lib.asr_op_linear_fp8_check(workspace.data_ptr(), st))
     return out
 
 
@@ -619,7 +629,8 @@ def cross_attention(q, k, v, cu_q, cu_k, max_q=None, max_k=None, out=None, works
     product over all layers), cu_q / cu_k int32 CUDA [n_seg+1] -> [Tq, H*64] (asr_op_cross_attention).  Without
     max_q / max_k they are read from the device, behind what `stream` holds (a synchronisation with it).  Rows outside every segment are not
     written (out keeps what it held).  workspace: a zeroed CUDA tensor of asr_op_cross_attention_ws_size()
-    bytes; with check the call synchronises and raises on bad offsets."""
+    bytes; with check the call synchronises and raises on bad offsets or a device wait that gave up (without it, a
+    program keeps a workspace and looks at its first int32: nothing else tells)."""
     torch = _t()
     dev, n_seg, max_q, max_k, Tq, Tk, H, Hkv, ldq, ldk, ldv = _cross_operands("cross_attention", q, k, v, cu_q, cu_k,
                                                                               max_q, max_k, out, workspace, stream)

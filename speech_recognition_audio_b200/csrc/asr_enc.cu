@@ -1872,6 +1872,19 @@ asr_status asr_op_quantize_fp8(const void* x, int x_dtype, int64_t ldx, int64_t 
   return ASR_OK;
 }
 
+// Synchronises `st` and turns a sticky status word into an asr_status;
+// `offsets` names what code 7 reports.
+static asr_status check_status_word(const char* who, const void* ws, void* stream, const char* offsets) {
+  if (!ws) return fail(nullptr, ASR_E_INVAL, "%s_check: workspace is NULL", who);
+  int code = 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ASR_CUDA(nullptr, cudaMemcpyAsync(&code, ws, 4, cudaMemcpyDeviceToHost, st));
+  ASR_CUDA(nullptr, cudaStreamSynchronize(st));
+  if (code == DEV_OK) return ASR_OK;
+  if (code == DEV_BAD_SEGMENT && offsets) return fail(nullptr, ASR_E_INVAL, "%s: %s", who, offsets);
+  return fail(nullptr, ASR_E_DEVICE_TIMEOUT, "%s: a bounded device wait gave up (code %d)", who, code);
+}
+
 size_t asr_op_linear_fp8_ws_size(void) { return 256; }
 
 asr_status asr_op_linear_fp8(const void* x, const void* xs, const void* w, const void* ws, const float* bias,
@@ -1910,6 +1923,10 @@ asr_status asr_op_linear_fp8(const void* x, const void* xs, const void* w, const
   ASR_CUDA(nullptr, launch_linear_fp8(x, static_cast<const uint8_t*>(xs), w, static_cast<const uint8_t*>(ws), p, e_bits,
                                       epi == ASR_EPI_F16, current_sm_count(), static_cast<cudaStream_t>(stream)));
   return ASR_OK;
+}
+
+asr_status asr_op_linear_fp8_check(const void* scratch, void* stream) {
+  return check_status_word("linear_fp8", scratch, stream, nullptr);
 }
 
 size_t asr_op_cross_attention_ws_size(void) { return 256; }
@@ -1964,16 +1981,8 @@ asr_status asr_op_cross_attention(const void* q, int64_t ldq, const void* k, int
 }
 
 asr_status asr_op_cross_attention_check(const void* ws, void* stream) {
-  if (!ws) return fail(nullptr, ASR_E_INVAL, "cross_attention_check: workspace is NULL");
-  int code = 0;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  ASR_CUDA(nullptr, cudaMemcpyAsync(&code, ws, 4, cudaMemcpyDeviceToHost, st));
-  ASR_CUDA(nullptr, cudaStreamSynchronize(st));
-  if (code == DEV_OK) return ASR_OK;
-  if (code == DEV_BAD_SEGMENT)
-    return fail(nullptr, ASR_E_INVAL, "cross_attention: segment offsets outside the arrays or longer than max_q / max_k, "
-                                      "or a head outside [0, H)");
-  return fail(nullptr, ASR_E_DEVICE_TIMEOUT, "cross_attention: a bounded device wait gave up (code %d)", code);
+  return check_status_word("cross_attention", ws, stream,
+                           "segment offsets outside the arrays or longer than max_q / max_k, or a head outside [0, H)");
 }
 
 asr_status asr_op_cross_attention_weights(const void* q, int64_t ldq, const void* k, int64_t ldk, const int32_t* cu_q,
