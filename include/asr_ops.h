@@ -164,7 +164,8 @@ asr_status asr_op_gelu(const float* x, float* y, int64_t n, void* stream);
  *             byte = s + 127.
  * Limits: M, K >= 1, K % 16 == 0, ldx >= K with rows of whole 16 bytes, x and
  * codes 16-byte aligned (ASR_E_INVAL otherwise); at most 2^31 - 1 blocks of
- * 1 x 128 (ASR_E_UNSUPPORTED).  Allocates nothing, asynchronous. */
+ * 1 x 128, K at most 2^31 - 256 (ASR_E_UNSUPPORTED).  Allocates nothing,
+ * asynchronous. */
 asr_status asr_op_quantize_fp8(const void* x, int x_dtype, int64_t ldx, int64_t M, int K, int block_rows, void* codes,
                                void* scales, void* stream);
 
@@ -189,7 +190,8 @@ asr_status asr_op_quantize_fp8(const void* x, int x_dtype, int64_t ldx, int64_t 
  *          synchronises the stream and turns the word into ASR_OK or
  *          ASR_E_DEVICE_TIMEOUT.
  * Limits: M >= 1, K % 16 == 0, N % 16 == 0 (SwiGLU: N % 32 == 0), operands
- * 16-byte aligned.  A NaN code or scale makes the outputs of its row or
+ * 16-byte aligned, M at most 2^31 - 256 (ASR_E_INVAL); N and K at most
+ * 2^31 - 256 (ASR_E_UNSUPPORTED).  A NaN code or scale makes the outputs of its row or
  * column NaN. */
 enum { ASR_EPI_F16 = 5 };
 size_t asr_op_linear_fp8_ws_size(void);

@@ -1866,7 +1866,7 @@ asr_status asr_op_quantize_fp8(const void* x, int x_dtype, int64_t ldx, int64_t 
     return fail(nullptr, ASR_E_INVAL, "quantize_fp8: unknown element type %d", x_dtype);
   if (block_rows != 1 && block_rows != 128)
     return fail(nullptr, ASR_E_INVAL, "quantize_fp8: block_rows must be 1 or 128");
-  if (M > 0x7FFFFFFF / ((K + 127) / 128)) return fail(nullptr, ASR_E_UNSUPPORTED, "quantize_fp8: too many blocks");
+  if (K > 0x7FFFFF00 || M > 0x7FFFFFFF / ((K + 127) / 128)) return fail(nullptr, ASR_E_UNSUPPORTED, "quantize_fp8: too many blocks");
   ASR_CUDA(nullptr, launch_quantize_fp8(x, x_dtype, ldx, M, K, block_rows, static_cast<uint8_t*>(codes),
                                         static_cast<uint8_t*>(scales), static_cast<cudaStream_t>(stream)));
   return ASR_OK;
@@ -1892,6 +1892,8 @@ asr_status asr_op_linear_fp8(const void* x, const void* xs, const void* w, const
                              void* stream) {
   if (!x || !xs || !w || !ws || !y || M <= 0 || N <= 0 || K <= 0 || K % 16 || N % 16 || M > 0x7FFFFF00)
     return fail(nullptr, ASR_E_INVAL, "linear_fp8: bad arguments (K %% 16, N %% 16)");
+  // a last tile's coordinates, rounded up to whole tiles, stay within 32 bits
+  if (N > 0x7FFFFF00 || K > 0x7FFFFF00) return fail(nullptr, ASR_E_UNSUPPORTED, "linear_fp8: N or K beyond 2^31 - 256");
   if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(y)) & 15)
     return fail(nullptr, ASR_E_INVAL, "linear_fp8: operands must be 16-byte aligned");
   if (!scratch || scratch_bytes < asr_op_linear_fp8_ws_size() || (reinterpret_cast<uintptr_t>(scratch) & 3))

@@ -17,6 +17,17 @@ def _linear(**change):
     return sra.lib.asr_op_linear_fp8(OK, OK, OK, OK, a["bias"], a["M"], a["N"], a["K"], 0, OK, OK, 256, None)
 
 
+@pytest.mark.parametrize("change,code", [(dict(N=TOP), UNSUPPORTED), (dict(K=TOP), UNSUPPORTED),
+                                         (dict(N=TOP - 0xE0), UNSUPPORTED), (dict(K=TOP - 0xE0), UNSUPPORTED)])
+def test_linear_fp8_limits(change, code):
+    assert _linear(**change) == code and b"linear_fp8" in sra.lib.asr_enc_last_error(None)
+
+
+def test_quantize_fp8_limits():
+    assert sra.lib.asr_op_quantize_fp8(OK, 0, TOP, 1, TOP, 1, OK, OK, None) == UNSUPPORTED
+    assert b"quantize_fp8" in sra.lib.asr_enc_last_error(None)
+
+
 def _cross(cq=OK, ck=OK):
     return sra.lib.asr_op_cross_attention(OK, 128, OK, 128, OK, 128, cq, ck, 1, 4, 4, 4, 4, 2, 2, 0, OK, 128, OK, 256, None)
 
