@@ -177,7 +177,7 @@ asr_status asr_op_quantize_fp8(const void* x, int x_dtype, int64_t ldx, int64_t 
  *          asr_op_quantize_fp8 writes them with block_rows 1.
  *  w, ws   e4m3 codes [N, K] and E8M0 scales [ceil(N / 128), ceil(K / 128)]
  *          (block_rows 128).
- *  bias    device float32 [N] or NULL.
+ *  bias    device float32 [N], 4-byte aligned (else ASR_E_INVAL), or NULL.
  *  epi     ASR_EPI_BF16, ASR_EPI_BF16_GELU, ASR_EPI_F32_RESID, ASR_EPI_F32 or
  *          ASR_EPI_SWIGLU as for asr_op_linear, or ASR_EPI_F16: y f16 [M, N] =
  *          acc + bias.
@@ -225,8 +225,9 @@ asr_status asr_op_linear_fp8_check(const void* scratch, void* stream);
  *         one stream or several may share it.  asr_op_cross_attention_check()
  *         synchronises the stream and turns the word into ASR_OK, ASR_E_INVAL
  *         or ASR_E_DEVICE_TIMEOUT.
- * Limits: H % Hkv == 0, strides multiples of 8 elements and at least the row
- * width, pointers 16-byte aligned (ASR_E_INVAL); H <= 65535, max_q * G <=
+ * Limits: n_seg >= 1, H % Hkv == 0, strides multiples of 8 elements and at
+ * least the row width, q, k, v and out 16-byte aligned, cu_q and cu_k 4-byte
+ * aligned (ASR_E_INVAL); H <= 65535, max_q * G <=
  * 1048560 and n_seg * ceil(max_q / 128) < 2^28 (ASR_E_UNSUPPORTED).  Tq == 0 or
  * max_q == 0 does nothing.
  * Results do not depend on timing: the parts of a split row are joined in a
@@ -244,7 +245,7 @@ asr_status asr_op_cross_attention_check(const void* ws, void* stream);
  *                      (q[i, heads[s]] . k[n, heads[s] / G] / 8)
  * in fp32, n counted from the segment's first state.  Columns n from the
  * segment's states to max_k are zero; rows outside every segment are left.
- *  heads    device int32 [n_sel], the query heads wanted, n_sel <= 65535 (a
+ *  heads    device int32 [n_sel], 4-byte aligned, the query heads wanted, n_sel <= 65535 (a
  *           value outside [0, H) sets the status word to 7 and writes
  *           nothing), or NULL with n_sel == H: all heads in order.
  *  weights  device float32 [n_sel, Tq, ldw], ldw >= max_k (rows of whole 32

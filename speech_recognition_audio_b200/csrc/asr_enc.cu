@@ -1896,6 +1896,7 @@ asr_status asr_op_linear_fp8(const void* x, const void* xs, const void* w, const
   if (N > 0x7FFFFF00 || K > 0x7FFFFF00) return fail(nullptr, ASR_E_UNSUPPORTED, "linear_fp8: N or K beyond 2^31 - 256");
   if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(y)) & 15)
     return fail(nullptr, ASR_E_INVAL, "linear_fp8: operands must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(bias) & 3) return fail(nullptr, ASR_E_INVAL, "linear_fp8: bias must start on a float");
   if (!scratch || scratch_bytes < asr_op_linear_fp8_ws_size() || (reinterpret_cast<uintptr_t>(scratch) & 3))
     return fail(nullptr, ASR_E_WORKSPACE, "linear_fp8: workspace too small");
   int e_bits = 0;
@@ -1942,6 +1943,8 @@ static asr_status xattn_args(const char* who, XattnArgs& a, const void* q, int64
     return fail(nullptr, dtype == ASR_DTYPE_F32 ? ASR_E_UNSUPPORTED : ASR_E_INVAL, "%s: dtype must be bf16 or f16", who);
   if (Tq < 0 || Tk < 0 || n_seg <= 0 || max_q < 0 || max_k < 0 || H <= 0 || Hkv <= 0 || H % Hkv || !cu_q || !cu_k)
     return fail(nullptr, ASR_E_INVAL, "%s: bad arguments", who);
+  if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k)) & 3)
+    return fail(nullptr, ASR_E_INVAL, "%s: cu_q and cu_k must start on an int32", who);
   if (!ws || ws_bytes < asr_op_cross_attention_ws_size() || (reinterpret_cast<uintptr_t>(ws) & 3))
     return fail(nullptr, ASR_E_WORKSPACE, "%s: workspace too small", who);
   // grid dimensions: (segments x row tiles x splits, heads or row tiles, heads)
@@ -1997,6 +2000,8 @@ asr_status asr_op_cross_attention_weights(const void* q, int64_t ldq, const void
   if (r != ASR_OK) return r;
   if (n_sel <= 0 || n_sel > 65535 || (!heads && n_sel != H) || ldw < max_k || (reinterpret_cast<uintptr_t>(weights) & 3))
     return fail(nullptr, ASR_E_INVAL, "cross_attention_weights: need n_sel heads (or all H) and ldw >= max_k");
+  if (reinterpret_cast<uintptr_t>(heads) & 3)
+    return fail(nullptr, ASR_E_INVAL, "cross_attention_weights: heads must start on an int32");
   if (Tq == 0 || max_q == 0 || max_k == 0) return ASR_OK;
   a.heads = heads;
   a.width = max_k;

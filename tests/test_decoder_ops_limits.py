@@ -18,7 +18,8 @@ def _linear(**change):
 
 
 @pytest.mark.parametrize("change,code", [(dict(N=TOP), UNSUPPORTED), (dict(K=TOP), UNSUPPORTED),
-                                         (dict(N=TOP - 0xE0), UNSUPPORTED), (dict(K=TOP - 0xE0), UNSUPPORTED)])
+                                         (dict(N=TOP - 0xE0), UNSUPPORTED), (dict(K=TOP - 0xE0), UNSUPPORTED),
+                                         (dict(bias=ODD), INVAL)])
 def test_linear_fp8_limits(change, code):
     assert _linear(**change) == code and b"linear_fp8" in sra.lib.asr_enc_last_error(None)
 
@@ -35,6 +36,12 @@ def _cross(cq=OK, ck=OK):
 def _weights(cq=OK, ck=OK, heads=OK, mk=4, ldw=8):
     return sra.lib.asr_op_cross_attention_weights(OK, 128, OK, 128, cq, ck, 1, 4, mk, 4, 4, 2, 2, 0, heads, 2, OK, ldw, OK,
                                                   256, None)
+
+
+@pytest.mark.parametrize("call", [lambda: _cross(cq=ODD), lambda: _cross(ck=ODD), lambda: _weights(cq=ODD),
+                                  lambda: _weights(ck=ODD), lambda: _weights(heads=ODD)])
+def test_offsets_and_heads_start_on_a_word(call):
+    assert call() == INVAL and b"cross_attention" in sra.lib.asr_enc_last_error(None)
 
 
 def test_fp8_check_needs_a_workspace():
