@@ -1980,6 +1980,7 @@ asr_status asr_op_cross_attention(const void* q, int64_t ldq, const void* k, int
   if ((Tk > 0 && !v) || (Tq > 0 && ((reinterpret_cast<uintptr_t>(out) & 15) || ldo < 64LL * H || ldo % 8)))
     return fail(nullptr, ASR_E_INVAL, "cross_attention: out must have aligned rows of H * 64 elements, and v be given");
   if (Tq == 0 || max_q == 0) return ASR_OK;
+  max_k = (int)std::min<int64_t>(max_k, Tk);  // no segment is longer
   ASR_CUDA(nullptr, launch_xattn(a, n_seg, max_k, dtype == ASR_DTYPE_F16, current_sm_count(),
                                  static_cast<cudaStream_t>(stream)));
   return ASR_OK;
@@ -2000,6 +2001,8 @@ asr_status asr_op_cross_attention_weights(const void* q, int64_t ldq, const void
   if (r != ASR_OK) return r;
   if (n_sel <= 0 || n_sel > 65535 || (!heads && n_sel != H) || ldw < max_k || (reinterpret_cast<uintptr_t>(weights) & 3))
     return fail(nullptr, ASR_E_INVAL, "cross_attention_weights: need n_sel heads (or all H) and ldw >= max_k");
+  // the kernels step past the last column, by a block's 256 columns at most
+  if (max_k > 0x7FFF0000) return fail(nullptr, ASR_E_UNSUPPORTED, "cross_attention_weights: max_k beyond 2^31 - 65536");
   if (reinterpret_cast<uintptr_t>(heads) & 3)
     return fail(nullptr, ASR_E_INVAL, "cross_attention_weights: heads must start on an int32");
   if (Tq == 0 || max_q == 0 || max_k == 0) return ASR_OK;

@@ -44,6 +44,11 @@ def test_offsets_and_heads_start_on_a_word(call):
     assert call() == INVAL and b"cross_attention" in sra.lib.asr_enc_last_error(None)
 
 
+@pytest.mark.parametrize("mk", [0x7FFFFFFF, 0x7FFF0001])
+def test_weights_of_more_columns_than_the_steps_can_count(mk):
+    assert _weights(mk=mk, ldw=1 << 31) == UNSUPPORTED and b"cross_attention" in sra.lib.asr_enc_last_error(None)
+
+
 def test_fp8_check_needs_a_workspace():
     assert sra.lib.asr_op_linear_fp8_check(None, None) == INVAL
     assert b"linear_fp8" in sra.lib.asr_enc_last_error(None)

@@ -55,3 +55,12 @@ def test_fp8_without_a_workspace_in_a_graph():
         y = sra.linear_fp8(*x, *w)
     graph.replay()
     assert torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("tq", [2, 50])
+def test_any_max_k_of_an_attention(tq):
+    """max_k only steers how the work is split, up to the largest int."""
+    q, k, v = _qkv(tq, 700)
+    cq, ck = _cu(0, tq), _cu(0, 700)
+    ref = sra.cross_attention(q, k, v, cq, ck)
+    assert torch.equal(sra.cross_attention(q, k, v, cq, ck, max_q=tq, max_k=2 ** 31 - 1), ref)
