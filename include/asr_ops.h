@@ -253,7 +253,8 @@ asr_status asr_op_cross_attention_check(const void* ws, void* stream);
  *           columns from max_k to ldw are not touched.
  *  max_k    at least the longest segment's states (a longer one sets the
  *           status word to 7 and is not written), at most 2^31 - 65536
- *           (ASR_E_UNSUPPORTED).
+ *           (ASR_E_UNSUPPORTED).  0: no columns, weights may be NULL, and
+ *           segments and heads are checked all the same.
  * Everything else as for asr_op_cross_attention. */
 asr_status asr_op_cross_attention_weights(const void* q, int64_t ldq, const void* k, int64_t ldk, const int32_t* cu_q,
                                           const int32_t* cu_k, int n_seg, int max_q, int max_k, int64_t Tq, int64_t Tk,

@@ -1952,7 +1952,7 @@ static asr_status xattn_args(const char* who, XattnArgs& a, const void* q, int64
       ((long long)max_q + 127) / 128 * 8 * n_seg > 0x7FFFFFFF)
     return fail(nullptr, ASR_E_UNSUPPORTED, "%s: sizes beyond the limits", who);
   const int64_t wq = 64LL * H, wk = 64LL * Hkv;
-  if (Tq > 0 && (!q || !out || (reinterpret_cast<uintptr_t>(q) & 15) || ldq < wq || ldq % 8))
+  if (Tq > 0 && (!q || (reinterpret_cast<uintptr_t>(q) & 15) || ldq < wq || ldq % 8))
     return fail(nullptr, ASR_E_INVAL, "%s: q must have aligned rows of H * 64 elements", who);
   if (Tk > 0 && (!k || (reinterpret_cast<uintptr_t>(k) & 15) || ldk < wk || ldk % 8 || (reinterpret_cast<uintptr_t>(v) & 15) ||
                  (v && (ldv < wk || ldv % 8))))
@@ -1963,6 +1963,7 @@ static asr_status xattn_args(const char* who, XattnArgs& a, const void* q, int64
   a.cu_q = cu_q, a.cu_k = cu_k;
   a.Tq = Tq, a.Tk = Tk;
   a.max_q = max_q, a.H = H, a.G = H / Hkv;
+  a.width = -1;
   a.out = out;
   a.status = static_cast<int*>(ws);
   a.limit_ns = kWaitLimitNs;
@@ -1977,7 +1978,7 @@ asr_status asr_op_cross_attention(const void* q, int64_t ldq, const void* k, int
   const asr_status r = xattn_args("cross_attention", a, q, ldq, k, ldk, v, ldv, cu_q, cu_k, n_seg, max_q, max_k, Tq, Tk,
                                   H, Hkv, dtype, out, ldo, ws, ws_bytes);
   if (r != ASR_OK) return r;
-  if ((Tk > 0 && !v) || (Tq > 0 && ((reinterpret_cast<uintptr_t>(out) & 15) || ldo < 64LL * H || ldo % 8)))
+  if ((Tk > 0 && !v) || (Tq > 0 && (!out || (reinterpret_cast<uintptr_t>(out) & 15) || ldo < 64LL * H || ldo % 8)))
     return fail(nullptr, ASR_E_INVAL, "cross_attention: out must have aligned rows of H * 64 elements, and v be given");
   if (Tq == 0 || max_q == 0) return ASR_OK;
   max_k = (int)std::min<int64_t>(max_k, Tk);  // no segment is longer
@@ -1999,13 +2000,14 @@ asr_status asr_op_cross_attention_weights(const void* q, int64_t ldq, const void
   const asr_status r = xattn_args("cross_attention_weights", a, q, ldq, k, ldk, nullptr, 0, cu_q, cu_k, n_seg, max_q,
                                   max_k, Tq, Tk, H, Hkv, dtype, weights, ldw, ws, ws_bytes);
   if (r != ASR_OK) return r;
-  if (n_sel <= 0 || n_sel > 65535 || (!heads && n_sel != H) || ldw < max_k || (reinterpret_cast<uintptr_t>(weights) & 3))
+  if (n_sel <= 0 || n_sel > 65535 || (!heads && n_sel != H) || ldw < max_k ||
+      (!weights && Tq > 0 && max_k > 0) || (reinterpret_cast<uintptr_t>(weights) & 3))
     return fail(nullptr, ASR_E_INVAL, "cross_attention_weights: need n_sel heads (or all H) and ldw >= max_k");
   // the kernels step past the last column, by a block's 256 columns at most
   if (max_k > 0x7FFF0000) return fail(nullptr, ASR_E_UNSUPPORTED, "cross_attention_weights: max_k beyond 2^31 - 65536");
   if (reinterpret_cast<uintptr_t>(heads) & 3)
     return fail(nullptr, ASR_E_INVAL, "cross_attention_weights: heads must start on an int32");
-  if (Tq == 0 || max_q == 0 || max_k == 0) return ASR_OK;
+  if (Tq == 0 || max_q == 0) return ASR_OK;
   a.heads = heads;
   a.width = max_k;
   ASR_CUDA(nullptr, launch_xattn_weights(a, n_seg, n_sel, dtype == ASR_DTYPE_F16, current_sm_count(),

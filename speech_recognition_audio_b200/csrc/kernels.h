@@ -183,7 +183,7 @@ struct XattnArgs {
   const int* heads;            // weights: the selected heads
   long long Tq, Tk;            // rows of q and of k / v
   int max_q, H, G;             // longest segment of rows, query heads, query heads per key head
-  int width;                   // weights: columns of a row (0 for the attention)
+  int width;                   // weights: columns of a row, no segment has more states (-1 for the attention)
   void* out;
   int* status;
   int splits;                  // set by the launcher

@@ -469,8 +469,9 @@ cudaError_t launch_xattn(XattnArgs a, int n_seg, int max_k, bool f16, int num_sm
   return f16 ? launch_rows<KIND_F16, 2>(a, n_seg, max_k, num_sms, st) : launch_rows<KIND_BF16, 2>(a, n_seg, max_k, num_sms, st);
 }
 
+// Without columns only the segments and heads are checked, which any kernel does.
 cudaError_t launch_xattn_weights(XattnArgs a, int n_seg, int n_sel, bool f16, int num_sms, cudaStream_t st) {
-  if (a.max_q > 32 && a.Tk > 0) return launch_xattn_weights_tiles(a, n_seg, n_sel, f16, num_sms, st);
+  if (a.max_q > 32 && a.Tk > 0 && a.width > 0) return launch_xattn_weights_tiles(a, n_seg, n_sel, f16, num_sms, st);
   const int tiles = (a.max_q + 15) / 16;
   a.splits = pick_splits((long long)n_seg * tiles * n_sel, a.width, XW_WARPS * XW_KEYS, num_sms);
   const dim3 grid(n_seg * a.splits, tiles, n_sel);

@@ -24,7 +24,7 @@ __device__ __forceinline__ Segment load_segment(const XattnArgs& a, int seg, boo
   s.lq = q1 - s.q0;
   s.lk = k1 - s.k0;
   s.ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= a.Tq && s.k0 >= 0 && k1 >= s.k0 && k1 <= a.Tk && s.lq <= a.max_q &&
-         (a.width == 0 || s.lk <= a.width);
+         (a.width < 0 || s.lk <= a.width);
   if (!s.ok && report) atomicCAS(a.status, 0, DEV_BAD_SEGMENT);
   return s;
 }

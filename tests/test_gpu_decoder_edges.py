@@ -19,6 +19,22 @@ def _qkv(tq, tk, h=2, hkv=2, dtype=torch.bfloat16, seed=1):
     return r(tq, 64 * h), r(tk, 64 * hkv), r(tk, 64 * hkv)
 
 
+@pytest.mark.parametrize("tq", [3, 70])
+def test_weights_of_width_zero_are_checked(tq):
+    """No columns: right where no segment has states, and reported where one has, or a head is none."""
+    q, k, _ = _qkv(tq, 9)
+    none = _cu(0, 0, 0)
+    cq = _cu(0, 2, tq)
+    assert sra.cross_attention_weights(q, k, cq, none).shape == (2, tq, 0)
+    assert sra.cross_attention_weights(q, k[:0], cq, none).shape == (2, tq, 0)
+    assert sra.cross_attention_weights(q, k, cq, none, heads=_cu(1)).shape == (1, tq, 0)
+    with pytest.raises(sra.AsrError) as e:
+        sra.cross_attention_weights(q, k, cq, _cu(0, 4, 9), max_k=0)
+    assert e.value.code == 1
+    with pytest.raises(sra.AsrError):
+        sra.cross_attention_weights(q, k, cq, none, heads=_cu(2))
+
+
 def test_fp8_status_is_checked(monkeypatch):
     """A status word that says a wait gave up becomes an error: in the library's check, in the call with check,
     and in a call that makes the workspace itself."""
