@@ -228,8 +228,8 @@ asr_status asr_op_linear_fp8_check(const void* scratch, void* stream);
  * Limits: n_seg >= 1, H % Hkv == 0, strides multiples of 8 elements and at
  * least the row width, q, k, v and out 16-byte aligned, cu_q and cu_k 4-byte
  * aligned (ASR_E_INVAL); H <= 65535, max_q * G <=
- * 1048560 and n_seg * ceil(max_q / 128) < 2^28 (ASR_E_UNSUPPORTED).  Tq == 0 or
- * max_q == 0 does nothing.
+ * 1048560 and n_seg * ceil(max_q / 128) < 2^28 (ASR_E_UNSUPPORTED).  Tq == 0
+ * does nothing.
  * Results do not depend on timing: the parts of a split row are joined in a
  * fixed order. */
 size_t asr_op_cross_attention_ws_size(void);

@@ -1980,7 +1980,7 @@ asr_status asr_op_cross_attention(const void* q, int64_t ldq, const void* k, int
   if (r != ASR_OK) return r;
   if ((Tk > 0 && !v) || (Tq > 0 && (!out || (reinterpret_cast<uintptr_t>(out) & 15) || ldo < 64LL * H || ldo % 8)))
     return fail(nullptr, ASR_E_INVAL, "cross_attention: out must have aligned rows of H * 64 elements, and v be given");
-  if (Tq == 0 || max_q == 0) return ASR_OK;
+  if (Tq == 0) return ASR_OK;
   max_k = (int)std::min<int64_t>(max_k, Tk);  // no segment is longer
   ASR_CUDA(nullptr, launch_xattn(a, n_seg, max_k, dtype == ASR_DTYPE_F16, current_sm_count(),
                                  static_cast<cudaStream_t>(stream)));
@@ -2007,7 +2007,7 @@ asr_status asr_op_cross_attention_weights(const void* q, int64_t ldq, const void
   if (max_k > 0x7FFF0000) return fail(nullptr, ASR_E_UNSUPPORTED, "cross_attention_weights: max_k beyond 2^31 - 65536");
   if (reinterpret_cast<uintptr_t>(heads) & 3)
     return fail(nullptr, ASR_E_INVAL, "cross_attention_weights: heads must start on an int32");
-  if (Tq == 0 || max_q == 0) return ASR_OK;
+  if (Tq == 0) return ASR_OK;
   a.heads = heads;
   a.width = max_k;
   ASR_CUDA(nullptr, launch_xattn_weights(a, n_seg, n_sel, dtype == ASR_DTYPE_F16, current_sm_count(),

@@ -441,7 +441,8 @@ __global__ void __launch_bounds__(32 * XW_WARPS, 2) xattn_weights_kernel(const X
 // tiles at 30000 keys 16x8 19.3, 16x16 12.7.
 template <int KIND, int NB>
 static cudaError_t launch_rows(XattnArgs a, int n_seg, int max_k, int num_sms, cudaStream_t st) {
-  const int tiles = (int)(((long long)a.max_q * a.G + 8 * NB - 1) / (8 * NB)), Hkv = a.H / a.G;
+  // at least one tile: a longest segment of no rows is checked, too
+  const int tiles = (int)std::max(((long long)a.max_q * a.G + 8 * NB - 1) / (8 * NB), 1LL), Hkv = a.H / a.G;
   const long long blocks = (long long)n_seg * tiles * Hkv, want = 10LL * num_sms;
   int W = 4;
   while (W < (NB == 1 ? 16 : 8) && blocks * W < want) W *= 2;
@@ -472,7 +473,7 @@ cudaError_t launch_xattn(XattnArgs a, int n_seg, int max_k, bool f16, int num_sm
 // Without columns only the segments and heads are checked, which any kernel does.
 cudaError_t launch_xattn_weights(XattnArgs a, int n_seg, int n_sel, bool f16, int num_sms, cudaStream_t st) {
   if (a.max_q > 32 && a.Tk > 0 && a.width > 0) return launch_xattn_weights_tiles(a, n_seg, n_sel, f16, num_sms, st);
-  const int tiles = (a.max_q + 15) / 16;
+  const int tiles = std::max((a.max_q + 15) / 16, 1);
   a.splits = pick_splits((long long)n_seg * tiles * n_sel, a.width, XW_WARPS * XW_KEYS, num_sms);
   const dim3 grid(n_seg * a.splits, tiles, n_sel);
   return f16 ? launch_cluster(xattn_weights_kernel<KIND_F16>, grid, 32 * XW_WARPS, 0, a.splits, st, a)

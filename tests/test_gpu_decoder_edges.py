@@ -35,6 +35,29 @@ def test_weights_of_width_zero_are_checked(tq):
         sra.cross_attention_weights(q, k, cq, none, heads=_cu(2))
 
 
+@pytest.mark.parametrize("op", ["attention", "weights"])
+def test_a_longest_segment_of_zero_rows_is_checked(op):
+    """max_q 0 is right where every segment is empty, and reported where one is not; `out` stays as it was."""
+    q, k, v = _qkv(5, 9)
+    ck = _cu(0, 4, 9)
+
+    def call(cq, **kw):
+        if op == "attention":
+            out = torch.full_like(q, 3.0)
+            sra.cross_attention(q, k, v, cq, ck, max_k=5, out=out, **kw)
+        else:
+            out = torch.full((2, 5, 5), 3.0, device="cuda")
+            sra.cross_attention_weights(q, k, cq, ck, max_k=5, out=out, **kw)
+        return out
+    for kw in ({}, {"max_q": 0}):
+        assert (call(_cu(2, 2, 2), **kw) == 3).all()
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    assert (call(_cu(0, 2, 5), max_q=0, workspace=ws, check=False) == 3).all()
+    assert int(ws.view(torch.int32)[0]) == 7
+    with pytest.raises(sra.AsrError):
+        call(_cu(0, 2, 5), max_q=0)
+
+
 def test_fp8_status_is_checked(monkeypatch):
     """A status word that says a wait gave up becomes an error: in the library's check, in the call with check,
     and in a call that makes the workspace itself."""
