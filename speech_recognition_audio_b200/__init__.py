@@ -500,12 +500,13 @@ def _raw_stream(stream, dev):
 
 
 def _rows(what, t):
-    """(rows, columns, row stride) of a 2-D tensor; refuses any whose rows are not contiguous."""
+    """(rows, columns, row stride) of a 2-D tensor; refuses any whose rows are not contiguous.  A single row has
+    no next one: its stride, whatever the matrix it is cut out of, is its width."""
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{what}: need 2-D tensors with contiguous rows")
     m, n = shape
-    return m, n, (stride[0] if m > 1 else max(stride[0], n))
+    return m, n, (stride[0] if m > 1 else n)
 
 
 def _on(stream):

@@ -58,6 +58,25 @@ def test_a_longest_segment_of_zero_rows_is_checked(op):
         call(_cu(0, 2, 5), max_q=0)
 
 
+def test_one_row_of_a_matrix_with_any_stride():
+    """A single row is read wherever it starts on 16 bytes, whatever the stride of the matrix it is cut out of."""
+    wide = torch.randn(4, 8 * 33 + 2, device="cuda")
+    x = wide[:1, :256]
+    assert x.stride(0) % 4
+    for block_rows in (1, 128):
+        got, ref = sra.quantize_fp8(x, block_rows), sra.quantize_fp8(x.clone(), block_rows)
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, ref))
+    q, k, v = _qkv(1, 1)
+    odd = lambda t: torch.nn.functional.pad(t, (0, 3, 0, 1))[:1, :t.shape[1]]  # noqa: E731
+    cq = ck = _cu(0, 1)
+    out = odd(torch.zeros_like(q))
+    assert out.stride(0) % 8
+    sra.cross_attention(odd(q), odd(k), odd(v), cq, ck, out=out)
+    assert torch.equal(out, v)  # one state: the probability is 1
+    w = sra.cross_attention_weights(odd(q), odd(k), cq, ck)
+    assert (w == 1).all()
+
+
 def test_fp8_status_is_checked(monkeypatch):
     """A status word that says a wait gave up becomes an error: in the library's check, in the call with check,
     and in a call that makes the workspace itself."""
