@@ -533,7 +533,7 @@ def _new(stream, shape, dtype, like, zero=False):
 def quantize_fp8(x, block_rows: int = 1, stream=None):
     """x CUDA [M, K] (bf16 / f16 / f32, rows may be strided) -> (codes float8_e4m3fn [M, K], scales
     float8_e8m0fnu [ceil(M / block_rows), ceil(K / 128)]), one power-of-two scale per block of block_rows
-    (1 or 128) x 128 (asr_op_quantize_fp8)."""
+    (1 or 128) x 128 (asr_op_quantize_fp8).  No rows give empty results."""
     torch = _t()
     dev = _operands("quantize_fp8", x)
     M, K, ldx = _rows("quantize_fp8", x)
@@ -542,6 +542,10 @@ def quantize_fp8(x, block_rows: int = 1, stream=None):
         raise ValueError(f"quantize_fp8: {x.dtype} is not bf16, f16 or f32")
     codes = _new(stream, (M, K), torch.float8_e4m3fn, x)
     scales = _new(stream, (-(-M // max(block_rows, 1)), -(-K // 128)), torch.float8_e8m0fnu, x)
+    if M == 0:
+        if K <= 0 or K % 16 or block_rows not in (1, 128):
+            raise AsrError(1, "quantize_fp8: bad arguments (K % 16, block_rows 1 or 128)")
+        return codes, scales
     _check(lib.asr_op_quantize_fp8(x.data_ptr(), code, ldx, M, K, block_rows, codes.data_ptr(), scales.data_ptr(),
                                    _raw_stream(stream, dev)))
     return codes, scales
@@ -550,7 +554,8 @@ def quantize_fp8(x, block_rows: int = 1, stream=None):
 def linear_fp8(x, x_scales, w, w_scales, bias=None, epi: int = EPI_BF16, out=None, workspace=None, stream=None,
                check=None):
     """Quantised x [M, K] and w [N, K] (float8_e4m3fn codes, float8_e8m0fnu scales: quantize_fp8(x) and
-    quantize_fp8(w, 128)), bias f32 [N] -> epilogue(x w^T + bias) (asr_op_linear_fp8).  workspace: a zeroed
+    quantize_fp8(w, 128)), bias f32 [N] -> epilogue(x w^T + bias) (asr_op_linear_fp8); no rows of x give an empty
+    result.  workspace: a zeroed
     CUDA tensor of asr_op_linear_fp8_ws_size() bytes whose first int32 the call sets if a device wait gives up;
     a program that calls this often keeps one and looks at it when it likes.  With check the call synchronises and
     raises on such a wait; None: where the call makes the workspace itself (a call that is being captured into a
@@ -579,6 +584,10 @@ def linear_fp8(x, x_scales, w, w_scales, bias=None, epi: int = EPI_BF16, out=Non
         out = _new(stream, shape, dt, x)
     elif out.dtype is not dt or out.shape != shape or not out.is_contiguous():
         raise ValueError(f"linear_fp8: out must be a contiguous {dt} tensor of shape {shape}")
+    if M == 0:
+        if K <= 0 or K % 16 or N <= 0 or N % (32 if epi == EPI_SWIGLU else 16) or not EPI_BF16 <= epi <= EPI_F16:
+            raise AsrError(1, "linear_fp8: bad arguments (K % 16, N % 16, epilogue)")
+        return out
     if workspace is None:
         workspace = _new(stream, (256,), torch.uint8, x, zero=True)
         if check is None:

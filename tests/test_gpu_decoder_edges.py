@@ -77,6 +77,35 @@ def test_one_row_of_a_matrix_with_any_stride():
     assert (w == 1).all()
 
 
+def test_no_rows_to_quantise_or_multiply():
+    w = sra.quantize_fp8(torch.randn(64, 256, device="cuda"), 128)
+    for dtype in (torch.float32, torch.bfloat16):
+        x = torch.randn(8, 256, device="cuda").to(dtype)[:0]
+        codes, scales = sra.quantize_fp8(x)
+        assert codes.shape == (0, 256) and codes.dtype == torch.float8_e4m3fn
+        assert scales.shape == (0, 2) and scales.dtype == torch.float8_e8m0fnu
+        for epi, shape, dt in ((sra.EPI_BF16, (0, 64), torch.bfloat16), (sra.EPI_SWIGLU, (0, 32), torch.bfloat16),
+                               (sra.EPI_F32, (0, 64), torch.float32)):
+            y = sra.linear_fp8(codes, scales, *w, epi=epi)
+            assert y.shape == shape and y.dtype == dt
+    assert sra.quantize_fp8(x, 128)[1].shape == (0, 2)
+    with pytest.raises(sra.AsrError):
+        sra.quantize_fp8(x, 64)
+    with pytest.raises(sra.AsrError):
+        sra.quantize_fp8(torch.zeros(0, 24, device="cuda"))
+    with pytest.raises(sra.AsrError):
+        sra.linear_fp8(codes, scales, *w, epi=9)
+
+
+@pytest.mark.parametrize("tq", [3, 60])
+def test_the_same_head_twice(tq):
+    q, k, _ = _qkv(tq, 300, 4, 2)
+    cq, ck = _cu(0, tq), _cu(0, 300)
+    all_heads = sra.cross_attention_weights(q, k, cq, ck)
+    got = sra.cross_attention_weights(q, k, cq, ck, heads=_cu(2, 2, 0, 2, 3))
+    assert torch.equal(got, all_heads[[2, 2, 0, 2, 3]])
+
+
 def test_fp8_status_is_checked(monkeypatch):
     """A status word that says a wait gave up becomes an error: in the library's check, in the call with check,
     and in a call that makes the workspace itself."""
