@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 16 / W : W == 4 ? 3 : 1) xat
     if (tok < s.lq) {
       const float inv = s.lk > 0 ? 1.0f / ll : 0.f;  // no states: zeros
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] *= inv;
+      for (int i = 0; i < 8; ++i) acc[i] = average<KIND>(acc[i], inv);
       *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + (long long)(s.q0 + tok) * a.ldo + 64 * h + e) =
           pack8_16<KIND>(acc);
     }

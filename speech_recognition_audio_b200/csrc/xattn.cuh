@@ -50,6 +50,17 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 // exp(-inf - m) is 0 there and not NaN.
 __device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.f : m; }
 
+// One output from its sum: an average of values of the type, so past the
+// type's largest only because the probabilities were rounded for the product
+// (a sum of theirs may exceed the one kept in 32 bits); infinities and NaN
+// stay what they are.
+template <int KIND>
+__device__ __forceinline__ float average(float sum, float inv) {
+  constexpr float top = KIND == KIND_F16 ? 65504.f : 3.3895313892515355e38f;
+  const float x = sum * inv;
+  return fabsf(x) < INFINITY ? fminf(fmaxf(x, -top), top) : x;
+}
+
 // Blocks a (segment, tile, head) is split into: a power of two, as long as the
 // grid does not yet fill `fill` blocks and each block keeps at least `least`
 // keys; up to `most` (8 is the portable cluster size, 16 needs allow_wide_clusters).

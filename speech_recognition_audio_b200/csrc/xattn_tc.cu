@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(XT_THREADS, 2)
       for (int c = 0; c < 4; ++c) {
         float o8[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o8[i] = ov[8 * c + i] * inv;
+        for (int i = 0; i < 8; ++i) o8[i] = average<KIND>(ov[8 * c + i], inv);
         dst[c] = pack8_16<KIND>(o8);
       }
     }

@@ -106,6 +106,30 @@ def test_the_same_head_twice(tq):
     assert torch.equal(got, all_heads[[2, 2, 0, 2, 3]])
 
 
+@pytest.mark.parametrize("tq", [2, 40])
+def test_the_largest_f16_values_stay_finite(tq):
+    """An average of values of at most 65504 is at most 65504, though rounded probabilities may sum to a little
+    more than their sum in 32 bits: of every 32 states one has weight 1 and 31 have p = 0.5003, which f16 rounds
+    up by a relative 4e-4."""
+    q, k, v = (torch.zeros(n, 64, dtype=torch.float16) for n in (tq, 1024, 1024))
+    q[:, :2] = 1.0
+    s = 8 * np.log(0.5 + 0.6 * 2.0 ** -11)
+    k[:, 0] = float(s)
+    k[:, 1] = float(s - k[0, 0].double().item())
+    k[::32] = 0
+    p = np.exp(k[1].double().sum().item() / 8)
+    up = float(np.float16(p)) - p
+    assert 31 * up / (1 + 31 * p) * 65504 > 20  # 65520 and more round to infinity
+    v += 65504
+    v[:, 1] = -65504
+    v[:, 2] = float("inf")
+    v[:, 3] = float("nan")
+    out = sra.cross_attention(q.cuda(), k.cuda(), v.cuda(), _cu(0, tq), _cu(0, 1024)).cpu()
+    finite = [c for c in range(64) if c not in (1, 2, 3)]
+    assert (out[:, finite] == 65504).all() and (out[:, 1] == -65504).all()
+    assert torch.isposinf(out[:, 2]).all() and torch.isnan(out[:, 3]).all()
+
+
 def test_fp8_status_is_checked(monkeypatch):
     """A status word that says a wait gave up becomes an error: in the library's check, in the call with check,
     and in a call that makes the workspace itself."""
