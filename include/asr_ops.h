@@ -230,6 +230,12 @@ asr_status asr_op_linear_fp8_check(const void* scratch, void* stream);
  * aligned (ASR_E_INVAL); H <= 65535, max_q * G <=
  * 1048560 and n_seg * ceil(max_q / 128) < 2^28 (ASR_E_UNSUPPORTED).  Tq == 0
  * does nothing.
+ * Arithmetic: scores, maxima, sums and outputs in fp32.  A probability, relative
+ * to its row's largest so far, is rounded to the values' type as an operand of
+ * its product with v (half a step, bf16 2^-8 or f16 2^-11 of it; in f16 what lies
+ * below 2^-25 of the largest counts in the sum only), as in the encoder's own
+ * 16-bit attention.  The products are summed before the division by the sum,
+ * so v's magnitude times the states must stay below 2^119 (bf16).
  * Results do not depend on timing: the parts of a split row are joined in a
  * fixed order. */
 size_t asr_op_cross_attention_ws_size(void);
