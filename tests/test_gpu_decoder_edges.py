@@ -168,6 +168,19 @@ def test_fp8_without_a_workspace_in_a_graph():
     assert torch.equal(y, ref)
 
 
+@pytest.mark.parametrize("up", [96, -96])
+def test_fp8_scales_of_opposite_extremes(up):
+    """The two scales of a block meet as one power of two: 2^up on one side and 2^-up on the other give the
+    bits of plain scales."""
+    torch.manual_seed(2)
+    xc, xs = sra.quantize_fp8(torch.randn(70, 400, device="cuda"))
+    wc, ws = sra.quantize_fp8(torch.randn(208, 400, device="cuda"), 128)
+    ref = sra.linear_fp8(xc, xs, wc, ws, epi=sra.EPI_F32)
+    shift = lambda s, by: (s.view(torch.uint8) + by).view(torch.float8_e8m0fnu)  # noqa: E731
+    got = sra.linear_fp8(xc, shift(xs, up), wc, shift(ws, -up), epi=sra.EPI_F32)
+    assert torch.equal(got, ref)
+
+
 @pytest.mark.parametrize("tq", [2, 50])
 def test_any_max_k_of_an_attention(tq):
     """max_k only steers how the work is split, up to the largest int."""
