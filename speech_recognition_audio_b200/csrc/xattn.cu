@@ -447,14 +447,13 @@ static cudaError_t launch_rows(XattnArgs a, int n_seg, int max_k, int num_sms, c
   int W = 4;
   while (W < (NB == 1 ? 16 : 8) && blocks * W < want) W *= 2;
   a.splits = pick_splits(blocks * W, max_k, 8 * W, want, W == 4 ? 8 : 16);
-  const dim3 grid(n_seg * a.splits, tiles, Hkv);
-  if (a.splits > 8) {
-    static std::atomic<unsigned long long> wide[2] = {{0}, {0}};
-    cudaError_t r = allow_wide_clusters(xattn_rows_kernel<KIND, NB, 8>, wide[0]);
+  static WideClusters seen[2];
+  a.splits = cap_splits(a.splits, [&] {
     if constexpr (NB == 1)
-      if (r == cudaSuccess) r = allow_wide_clusters(xattn_rows_kernel<KIND, NB, 16>, wide[1]);
-    if (r != cudaSuccess) return r;
-  }
+      if (W == 16) return holds_wide_cluster(xattn_rows_kernel<KIND, NB, 16>, 512, 0, seen[1]);
+    return holds_wide_cluster(xattn_rows_kernel<KIND, NB, 8>, 256, 0, seen[0]);
+  });
+  const dim3 grid(n_seg * a.splits, tiles, Hkv);
   if (W == 4) return launch_cluster(xattn_rows_kernel<KIND, NB, 4>, grid, 128, 0, a.splits, st, a);
   if (W == 8) return launch_cluster(xattn_rows_kernel<KIND, NB, 8>, grid, 256, 0, a.splits, st, a);
   if constexpr (NB == 1) return launch_cluster(xattn_rows_kernel<KIND, NB, 16>, grid, 512, 0, a.splits, st, a);

@@ -1,9 +1,10 @@
 // Shared by the cross-attention kernels: segment bounds, distributed shared
-// memory reads, and the launch of a grid whose clusters split the keys.
+// memory reads, and the clusters that a device can hold.
 #pragma once
 
 #include "gemm2.cuh"
 #include "kernels.h"
+#include "splits.h"
 
 namespace asr {
 
@@ -61,24 +62,37 @@ __device__ __forceinline__ float average(float sum, float inv) {
   return fabsf(x) < INFINITY ? fminf(fmaxf(x, -top), top) : x;
 }
 
-// Blocks a (segment, tile, head) is split into: a power of two, as long as the
-// grid does not yet fill `fill` blocks and each block keeps at least `least`
-// keys; up to `most` (8 is the portable cluster size, 16 needs allow_wide_clusters).
-inline int pick_splits(long long blocks, int keys, int least, long long fill, int most = 8) {
-  int s = 1;
-  while (s < most && blocks * s < fill && keys >= 2 * s * least) s *= 2;
-  return s;
-}
-// Lets a kernel be launched in clusters of 16, once per device.
+// Whether the current device can hold a cluster of 16 of these blocks, which
+// is more than the portable size; asked once per device (`known` and `wide`
+// are the caller's own masks of devices, one pair per kernel).
+struct WideClusters {
+  std::atomic<unsigned long long> known{0}, wide{0};
+};
 template <typename... KArgs>
-cudaError_t allow_wide_clusters(void (*kernel)(KArgs...), std::atomic<unsigned long long>& done) {
+bool holds_wide_cluster(void (*kernel)(KArgs...), int threads, size_t smem, WideClusters& seen) {
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const unsigned long long bit = 1ull << (dev & 63);
-  if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) & bit))) return e;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
+  if (dev < 64 && (seen.known.load(std::memory_order_acquire) & bit)) return seen.wide.load(std::memory_order_relaxed) & bit;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 16;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                  cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
+  if (!ok) cudaGetLastError();  // a refusal is an answer here, not an error of the call
+  if (dev < 64) {
+    if (ok) seen.wide.fetch_or(bit, std::memory_order_relaxed);
+    seen.known.fetch_or(bit, std::memory_order_release);
+  }
+  return ok;
 }
 
 }  // namespace asr

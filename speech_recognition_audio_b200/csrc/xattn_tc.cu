@@ -361,33 +361,16 @@ __global__ void __launch_bounds__(XT_THREADS, 2)
 }
 
 template <int KIND>
-static cudaError_t launch_tiles(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const XattnArgs& a,
+static cudaError_t launch_tiles(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, XattnArgs a,
                                 int n_seg, cudaStream_t st) {
   auto kern = xattn_tiles_kernel<KIND>;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = set_smem_once(kern, XT_SMEM, done);
   if (e != cudaSuccess) return e;
-  if (a.splits > 8) {
-    static std::atomic<unsigned long long> wide{0};
-    const cudaError_t r = allow_wide_clusters(kern, wide);
-    if (r != cudaSuccess) return r;
-  }
+  static WideClusters seen;
+  a.splits = cap_splits(a.splits, [&] { return holds_wide_cluster(kern, XT_THREADS, XT_SMEM, seen); });
   const int q_blocks = (a.max_q + 127) / 128;
   return launch_cluster(kern, dim3(n_seg * q_blocks * a.splits, a.H), XT_THREADS, XT_SMEM, a.splits, st, q, k, v, a, q_blocks);
-}
-
-// Splits S: a tile of states takes about 1.5 us a pass, and each block of a
-// cluster costs about 0.12 us to get going, so the S with the least
-// cost tiles / S + blocks S, cost = 12.5 a pass.  Measured (attention, us) at 1,
-// 8 and 16, or the most that leaves a block a tile: 4 blocks x 235 tiles 281,
-// 48, 33; 12 x 235 282, 51, 47; 12 x 63 80, 23, 25; 12 x 12 19, 14; 48 x 12 20,
-// 22; 96 x 12 20, 33.
-static int xt_splits(double blocks, int tiles, double cost, int num_sms) {
-  double least = cost * tiles;
-  int best = 1;
-  for (int S = 2; S <= 16 && S <= tiles && blocks * S <= 2 * num_sms; S *= 2)
-    if (cost * tiles / S + blocks * S < least) best = S, least = cost * tiles / S + blocks * S;
-  return best;
 }
 
 cudaError_t launch_xattn_tiles(XattnArgs a, int n_seg, int max_k, bool f16, int num_sms, cudaStream_t st) {
@@ -396,7 +379,7 @@ cudaError_t launch_xattn_tiles(XattnArgs a, int n_seg, int max_k, bool f16, int 
       !make_tmap_bf16(&k, a.k, a.Tk, 64ULL * (a.H / a.G), a.ldk, 128) ||
       !make_tmap_bf16(&v, a.v, a.Tk, 64ULL * (a.H / a.G), a.ldv, 128))
     return cudaErrorInvalidValue;
-  a.splits = xt_splits((double)n_seg * ((a.max_q + 127) / 128) * a.H, (max_k + 127) / 128, 12.5, num_sms);
+  a.splits = tile_splits((double)n_seg * ((a.max_q + 127) / 128) * a.H, (max_k + 127) / 128, 12.5, num_sms);
   return f16 ? launch_tiles<KIND_F16>(q, k, v, a, n_seg, st) : launch_tiles<KIND_BF16>(q, k, v, a, n_seg, st);
 }
 
@@ -665,16 +648,13 @@ cudaError_t launch_xattn_weights_tiles(XattnArgs a, int n_seg, int n_sel, bool f
   if (!tma) o = k;
   const int q_blocks = (a.max_q + 127) / 128;
   // as for the attention, with two passes over each tile
-  a.splits = xt_splits((double)n_seg * q_blocks * n_sel, (a.width + 127) / 128, 25.0, num_sms);
+  a.splits = tile_splits((double)n_seg * q_blocks * n_sel, (a.width + 127) / 128, 25.0, num_sms);
   auto kern = f16 ? xattn_weights_tiles_kernel<KIND_F16> : xattn_weights_tiles_kernel<KIND_BF16>;
   static std::atomic<unsigned long long> done[2] = {{0}, {0}};
   const cudaError_t e = set_smem_once(kern, XWT_SMEM, done[f16]);
   if (e != cudaSuccess) return e;
-  if (a.splits > 8) {
-    static std::atomic<unsigned long long> wide[2] = {{0}, {0}};
-    const cudaError_t r = allow_wide_clusters(kern, wide[f16]);
-    if (r != cudaSuccess) return r;
-  }
+  static WideClusters seen[2];
+  a.splits = cap_splits(a.splits, [&] { return holds_wide_cluster(kern, 320, XWT_SMEM, seen[f16]); });
   return launch_cluster(kern, dim3(n_seg * q_blocks * a.splits, n_sel), 320, XWT_SMEM, a.splits, st, q, k, o, a, q_blocks, (int)tma);
 }
 
