@@ -361,7 +361,7 @@ __device__ __forceinline__ void sf_copy(uint2* dst, const uint8_t* sc, long long
   }
 }
 __device__ __forceinline__ uint32_t sf_bytes(uint2 v, long long r, int KB) {
-  return __funnelshift_r(v.x, v.y, 8 * (static_cast<int>(r) * KB & 3));
+  return __funnelshift_r(v.x, v.y, 8 * static_cast<int>(r * KB & 3));
 }
 
 // Epilogue of one warp for 16-bit outputs: its 32 rows and COLS (64, or
