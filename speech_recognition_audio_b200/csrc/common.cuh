@@ -71,26 +71,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t addr, uint32_t parity) {
 // limit_ns of device time.  Also gives up early when the shared status word
 // already holds an error (another role or block gave up).  On giving up it
 // records `code` in *status and returns false.
-static __device__ __noinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
-                                               int* status, int code) {
-  const uint32_t a = smem_u32(bar);
-  if (mbar_try_wait(a, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 0;; ++it) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(a, parity)) return true;
-    const uint64_t now = globaltimer_ns();
-    if (now - t0 > limit_ns) {
-      if (status) atomicCAS(status, 0, code);
-      return false;
-    }
-    if (status && (it & 15) == 15 && *reinterpret_cast<volatile int*>(status) != 0) return false;
-  }
-}
-
-// The same wait inline: a call's register saves cost a single-warp issuer
-// about 350 cycles a wait, completed barriers included.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, int* status, int code) {
   const uint32_t a = smem_u32(bar);
   if (mbar_try_wait(a, parity)) return true;
@@ -105,6 +85,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
     }
     if (status && it % 512 == 0 && *reinterpret_cast<volatile int*>(status) != 0) return false;
   }
+}
+
+// The same wait as a call, which keeps kernels with many waits small.  A call's
+// register saves cost a single-warp issuer about 350 cycles a wait, completed
+// barriers included; such issuers take the inline form.
+static __device__ __noinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                               int* status, int code) {
+  return mbar_wait(bar, parity, limit_ns, status, code);
 }
 
 // --------------------------------------------------------------- TMA loads
@@ -162,6 +150,13 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_u32(bar))
                : "memory");
+}
+// The same by a whole warp in step: one elected lane commits what it issued.
+__device__ __forceinline__ void tc_commit_warp(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
 }
 // D[tmem] (+)= A[smem] * B[smem]^T, kind::f16 (bf16 inputs, fp32 accumulate).
 __device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,

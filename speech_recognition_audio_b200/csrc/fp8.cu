@@ -324,13 +324,6 @@ __device__ __forceinline__ void tc_mma4_mxf8(uint32_t d, uint64_t ad, uint64_t b
         "l"(bd + 4), "l"(ad + 6), "l"(bd + 6)
         : "memory");
 }
-// Commit of the elected lane's MMAs.
-__device__ __forceinline__ void tc_commit_elect(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
-}
 __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -512,17 +505,17 @@ __global__ void __launch_bounds__(Fp8Shape<BN, epi_wide<EPI>()>::THREADS, 1)
         const uint32_t sf = tmem + S::SF_BASE + slot * S::SF_COLS;
         tc_mma4_mxf8(d, ad0 + s * (S::A_BYTES >> 4), bd0 + s * (S::B_BYTES >> 4), idesc_sf(idesc, kb & 3), sf,
                             sf + S::SF_A, kb > 0 ? 1u : 0u);
-        tc_commit_elect(&empty[s]);
+        tc_commit_warp(&empty[s]);
         if ((kb & 3) == 3 || kb == p.k_blocks - 1) {
-          tc_commit_elect(&sempty[slot]);
+          tc_commit_warp(&sempty[slot]);
           ++sg;
         }
       }
       if (!ok) break;
-      tc_commit_elect(&tfull[a]);
+      tc_commit_warp(&tfull[a]);
     }
     // all issued MMAs complete before tensor memory is released
-    tc_commit_elect(drain);
+    tc_commit_warp(drain);
     mbar_wait(drain, 0, kDrainLimitNs, nullptr, 0);
   } else if (warp < 2 + S::EPI_WARPS) {
     const int q = warp & 3, part = (warp - 2) / 4;

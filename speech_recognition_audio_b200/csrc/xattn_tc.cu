@@ -91,12 +91,6 @@ __device__ __forceinline__ void tc_values_warp(uint32_t d_tmem, uint32_t a_tmem,
 // whole block, reached from different branches (id 5).
 __device__ __forceinline__ void pair_sync(int q) { asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory"); }
 __device__ __forceinline__ void block_sync() { asm volatile("bar.sync 5, %0;" ::"n"(XT_THREADS) : "memory"); }
-__device__ __forceinline__ void tc_commit_warp(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
-}
 
 }  // namespace
 
