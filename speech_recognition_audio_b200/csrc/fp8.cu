@@ -132,8 +132,8 @@ __device__ __forceinline__ uint2 codes8(const Raw8<DT>& r, int s, bool special) 
 
 // One scale per row and 128 columns.  Sixteen lanes share a block (eight
 // elements each: whole 16-byte loads and 8-byte code stores, a 128-byte
-// segment per block).  Bound by HBM: 28 us for 48000 x 768 fp32 (184 MB, the
-// copy rate), 19.5 for 6240 x 5120 bf16 (96 MB).
+// segment per block).  Bound by HBM: 27.6 us for 48000 x 768 fp32 (184 MB, the
+// copy rate), 19.0 for 6240 x 5120 bf16 (96 MB).
 template <int DT>
 __global__ void __launch_bounds__(QZ_THREADS) quantize_rows_kernel(const void* __restrict__ x, long long ldx, int K,
                                                                    int KB, unsigned int units,
@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(QZ_THREADS) quantize_rows_kernel(const void* _
 
 // One scale per 128 x 128 block (weights): one thread block each, the 128
 // rows in eight passes of sixteen, held in registers between the maximum and
-// the conversion.
+// the conversion.  Bound by HBM: 27.6 us for 16384 x 2048 fp32 (168 MB, 93 % of
+// the copy rate), 16.9 for bf16 (101 MB).
 template <int DT>
 __global__ void __launch_bounds__(QZ_THREADS) quantize_blocks_kernel(const void* __restrict__ x, long long ldx,
                                                                      long long M, int K, int KB,
@@ -309,9 +310,8 @@ __device__ __forceinline__ uint32_t idesc_sf(uint32_t idesc, int byte) {
   return idesc | (static_cast<uint32_t>(byte) << 4) | (static_cast<uint32_t>(byte) << 29);
 }
 // The four K = 32 steps of a 128-element k-block.  Written for a whole warp in
-// step, one elected lane issuing: the operands then stay in uniform registers
-// (a lone lane's are moved there for every instruction; 6240 x 1280 x 5120
-// took 86 us that way, 40 this way).
+// step, one elected lane issuing: 6240 x 1280 x 5120 took 40 us this way and
+// 86 with a branch that only one lane took.
 __device__ __forceinline__ void tc_mma4_mxf8(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
                                              uint32_t sfb, uint32_t accumulate) {
   asm volatile(
@@ -415,10 +415,14 @@ __device__ __forceinline__ void epilogue_wide(const GemmParams& p, const CUtenso
 // CTA in shared memory, and the CTA reports it to p.status at its end.
 //
 // What bounds it: a k-block of a 128 x 192 tile is 384 clocks of MMAs, 40 KB
-// into shared memory and 40 KB out of it again; it takes about 530.
-// 6240 x 2048 x 8192 runs at 2350 TFLOP/s (72 % of twice the measured bf16
-// rate), 48000 x 18432 x 768 (1.77 GB of output) at 1810, at 1.5 GHz under the
-// power cap.
+// into shared memory and 40 KB out of it again.  In a steady loop under the
+// power cap 6240 x 2048 x 8192 takes 99 us at 1.49 GHz: 2115 TFLOP/s (65 % of
+// twice the measured bf16 rate), 576 clocks a k-block over its four waves of
+// 64.  48000 x 18432 x 768 (1.77 GB of output) takes 815-840 us at 1.4 GHz,
+// 1640 TFLOP/s, and 750 in the first passes from idle: about 4800 clocks a
+// tile of six k-blocks, of which some 1300 are not the main loop's; where they
+// go has not been measured.  6240 x 1280 x 5120 with the residual takes 51 us
+// at 1.97 GHz, three waves of tiles where 2.3 would do.
 template <int BN, int EPI, int KIND>
 __global__ void __launch_bounds__(Fp8Shape<BN, epi_wide<EPI>()>::THREADS, 1)
     gemm_fp8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,

@@ -460,8 +460,19 @@ static cudaError_t launch_rows(XattnArgs a, int n_seg, int max_k, int num_sms, c
   return cudaErrorInvalidValue;
 }
 
-// Up to 32 rows (tokens) the rows kernel reads the states once per 16 rows;
-// beyond, the tiles of 128.
+// Up to 32 tokens the rows kernel, which reads the states once per 16 rows
+// (tokens x shared heads); beyond, the tiles of 128 tokens of one query head.
+// Both sides grow with the shared heads alike, so tokens alone decide.  On the
+// device, rows / tiles, us, at 1500 states:
+//   tokens                        16           32           48           64
+//   1 segment,  G = 1  12 heads   10.5 / 13.7  10.1 / 13.8  14.7 / 13.9  11.4 / 13.9
+//   8 segments, G = 1  12 heads   14.4 / 19.0  18.0 / 19.2  18.5 / 19.3  20.6 / 19.5
+//   32,         G = 1  12 heads   28.1 / 42.9  43.4 / 43.4  61.2 / 44.3  79.3 / 45.0
+//   32,         G = 5  20 heads   39.2 / 63.8  59.0 / 64.2  90.0 / 65.4  115 / 66.0
+//   8 segments, G = 8  16 heads   14.7 / 19.2  19.0 / 19.2  23.0 / 19.4  33.8 / 19.5
+//   32,         G = 8  16 heads   33.5 / 51.3  52.8 / 51.6  74.5 / 52.4  95.5 / 53.0
+// The longest segment decides for the whole call: one prompt takes the calls
+// of one token beside it along to the tiles.
 cudaError_t launch_xattn(XattnArgs a, int n_seg, int max_k, bool f16, int num_sms, cudaStream_t st) {
   if (a.max_q > 32 && a.Tk > 0) return launch_xattn_tiles(a, n_seg, max_k, f16, num_sms, st);
   if ((long long)a.max_q * a.G <= 8)
@@ -469,7 +480,11 @@ cudaError_t launch_xattn(XattnArgs a, int n_seg, int max_k, bool f16, int num_sm
   return f16 ? launch_rows<KIND_F16, 2>(a, n_seg, max_k, num_sms, st) : launch_rows<KIND_BF16, 2>(a, n_seg, max_k, num_sms, st);
 }
 
-// Without columns only the segments and heads are checked, which any kernel does.
+// The same border for the weights (12 heads of 1500 states, rows / tiles, us, at
+// 32, 48 and 64 tokens: 1 segment 6.4 / 12.1, 7.7 / 13.2, 7.9 / 12.3; 8 segments
+// 16.4 / 28.6, 16.4 / 33.0, 30.8 / 28.8; 32 segments 56.9 / 63.6, 73.6 / 73.6,
+// 90.8 / 69.3).  Without columns only the segments and heads are checked, which
+// any kernel does.
 cudaError_t launch_xattn_weights(XattnArgs a, int n_seg, int n_sel, bool f16, int num_sms, cudaStream_t st) {
   if (a.max_q > 32 && a.Tk > 0 && a.width > 0) return launch_xattn_weights_tiles(a, n_seg, n_sel, f16, num_sms, st);
   const int tiles = std::max((a.max_q + 15) / 16, 1);

@@ -14,10 +14,10 @@
 // Floors: 16 exponentials per clock and SM against 4096 products, so a tile of
 // 128 x 128 costs 1024 clocks of them and 512 of the tensor pipe.  2240 rows x
 // 1500 states x 12 heads x 32 segments (330 GFLOP, 1.29e9 exponentials = 277 us
-// at 1965 MHz): 602 us.  What bounds it is the chain of a step (wait, read,
-// maximum, exponentials, write, product), of which four softmax warps per
-// scheduler hide about half: without the exponentials it takes 479 us, without
-// them and the maxima 443.  Measured on the way there: single-lane issue with
+// at 1965 MHz): 608-613 us, 540 TFLOP/s.  What bounds it is the chain of a step
+// (wait, read, maximum, exponentials, write, product), of which four softmax
+// warps per scheduler hide about half: the exponential unit is 52 % busy, the
+// tensor pipe 25 %, issue 48 %.  Measured on the way there: single-lane issue with
 // waits behind a call 868; one thread a row and two tiles a block 617, with
 // the tiles' exponentials taking turns 762; exponentials ahead of the maximum,
 // repeated where it moved, 615; two independent streams of 64-state tiles a
@@ -59,9 +59,8 @@ static_assert(128 * (XT_PART_LD + 2) * 4 <= XT_RED, "parts fit in the tiles");
 static_assert(2 * (XT_SMEM + 1024) <= 228 * 1024, "two blocks per SM");
 
 // The tensor-core issue below is written for a whole warp in step: every lane
-// computes the same addresses (so they live in uniform registers, where a
-// lone lane's would be moved there one by one, about 75 cycles an
-// instruction) and one elected lane issues.
+// computes the same addresses and one elected lane issues.  The rescoring case
+// took 651 us this way and 719 with a branch that only one lane took.
 // S = Q K^T: the four K = 16 steps of 64 elements.
 __device__ __forceinline__ void tc_scores_warp(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc) {
   asm volatile(
@@ -383,8 +382,8 @@ cudaError_t launch_xattn_tiles(XattnArgs a, int n_seg, int max_k, bool f16, int 
 // every tile), joined over the two halves once at its end; the second turns
 // the same scores into probabilities, staged as 32 x 32 boxes and written by
 // TMA.  448 rows x 1500 states x 10 heads x 32 segments (942 MB, 144 us at the
-// copy rate; twice 46 us of exponentials): 230 us; 64 rows a block on mma.sync
-// took 402.
+// copy rate; twice 46 us of exponentials): 221-227 us; 64 rows a block on
+// mma.sync took 402.
 namespace {
 constexpr int XWT_KS = 2, XWT_SK = XT_TILE, XWT_BUF = XWT_SK + XWT_KS * XT_TILE, XWT_RED = XWT_BUF + 8 * 4096;
 constexpr int XWT_BARS = XWT_RED + 2 * 128 * 8;
