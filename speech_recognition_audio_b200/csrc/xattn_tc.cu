@@ -573,7 +573,8 @@ __global__ void __launch_bounds__(320, 2)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           dst[k ^ (lane & 7)] = make_float4(v[32 * b + 4 * k], v[32 * b + 4 * k + 1], v[32 * b + 4 * k + 2], v[32 * b + 4 * k + 3]);
-        if (out_tma && rows >= 32) {
+        // (a store clips a box at the width rounded up to whole 16 bytes)
+        if (out_tma && rows >= 32 && (x0 + 32 <= a.width || a.width % 4 == 0)) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -581,8 +582,8 @@ __global__ void __launch_bounds__(320, 2)
             bulk_commit();
           }
         } else {
-          // rows of the next segment follow inside the box, or rows are not
-          // whole 16 bytes: eight lanes a row
+          // rows of the next segment follow inside the box, or rows or the
+          // width are not whole 16 bytes: eight lanes a row
           __syncwarp();
 #pragma unroll 1
           for (int r = lane >> 3; r < min(32, rows); r += 4) {

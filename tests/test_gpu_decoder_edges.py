@@ -188,3 +188,15 @@ def test_any_max_k_of_an_attention(tq):
     cq, ck = _cu(0, tq), _cu(0, 700)
     ref = sra.cross_attention(q, k, v, cq, ck)
     assert torch.equal(sra.cross_attention(q, k, v, cq, ck, max_q=tq, max_k=2 ** 31 - 1), ref)
+
+
+@pytest.mark.parametrize("tokens", [5, 70])
+@pytest.mark.parametrize("n", [4, 61, 62, 63, 64, 130, 133])
+def test_columns_behind_the_width_keep_what_they_held(tokens, n):
+    """Rows of whole 32 bytes that are wider than max_k: the columns behind it are not written, whether or not
+    they start on 16 bytes."""
+    q, k = (torch.randn(m, 128, device="cuda").bfloat16() for m in (tokens, n))
+    buf = torch.full((2, tokens, 160), 9.0, device="cuda")
+    sra.cross_attention_weights(q, k, _cu(0, tokens), _cu(0, n), out=buf[:, :, :n])
+    assert torch.equal(buf[:, :, :n], sra.cross_attention_weights(q, k, _cu(0, tokens), _cu(0, n)))
+    assert (buf[:, :, n:] == 9).all()
