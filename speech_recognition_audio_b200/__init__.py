@@ -640,7 +640,8 @@ def cross_attention(q, k, v, cu_q, cu_k, max_q=None, max_k=None, out=None, works
     max_q / max_k they are read from the device, behind what `stream` holds (a synchronisation with it).  Rows outside every segment are not
     written (out keeps what it held).  workspace: a zeroed CUDA tensor of asr_op_cross_attention_ws_size()
     bytes; with check the call synchronises and raises on bad offsets or a device wait that gave up (without it, a
-    program keeps a workspace and looks at its first int32: nothing else tells)."""
+    program keeps a workspace and looks at its first int32: nothing else tells).  The word stays set until the
+    program zeroes it again."""
     torch = _t()
     dev, n_seg, max_q, max_k, Tq, Tk, H, Hkv, ldq, ldk, ldv = _cross_operands("cross_attention", q, k, v, cu_q, cu_k,
                                                                               max_q, max_k, out, workspace, stream)
