@@ -51,15 +51,15 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 // exp(-inf - m) is 0 there and not NaN.
 __device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.f : m; }
 
-// One output from its sum: an average of values of the type, so past the
-// type's largest only because the probabilities were rounded for the product
-// (a sum of theirs may exceed the one kept in 32 bits); infinities and NaN
-// stay what they are.
+// One output from its sum: an average of values of the type, so past f16's
+// largest only because the probabilities were rounded for the product (a sum
+// of theirs may exceed the one kept in 32 bits); infinities and NaN stay what
+// they are.  bf16 reaches as far as the fp32 sums themselves.
 template <int KIND>
 __device__ __forceinline__ float average(float sum, float inv) {
-  constexpr float top = KIND == KIND_F16 ? 65504.f : 3.3895313892515355e38f;
   const float x = sum * inv;
-  return fabsf(x) < INFINITY ? fminf(fmaxf(x, -top), top) : x;
+  if constexpr (KIND == KIND_F16) return fabsf(x) < INFINITY ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
+  return x;
 }
 
 // Whether the current device can hold a cluster of 16 of these blocks, which

@@ -14,7 +14,7 @@
 // Floors: 16 exponentials per clock and SM against 4096 products, so a tile of
 // 128 x 128 costs 1024 clocks of them and 512 of the tensor pipe.  2240 rows x
 // 1500 states x 12 heads x 32 segments (330 GFLOP, 1.29e9 exponentials = 277 us
-// at 1965 MHz): 608-613 us, 540 TFLOP/s.  What bounds it is the chain of a step
+// at 1965 MHz): 600-613 us, 540-550 TFLOP/s.  What bounds it is the chain of a step
 // (wait, read, maximum, exponentials, write, product), of which four softmax
 // warps per scheduler hide about half: the exponential unit is 52 % busy, the
 // tensor pipe 25 %, issue 48 %.  Measured on the way there: single-lane issue with
@@ -382,7 +382,7 @@ cudaError_t launch_xattn_tiles(XattnArgs a, int n_seg, int max_k, bool f16, int 
 // every tile), joined over the two halves once at its end; the second turns
 // the same scores into probabilities, staged as 32 x 32 boxes and written by
 // TMA.  448 rows x 1500 states x 10 heads x 32 segments (942 MB, 144 us at the
-// copy rate; twice 46 us of exponentials): 221-227 us; 64 rows a block on
+// copy rate; twice 46 us of exponentials): 221-231 us; 64 rows a block on
 // mma.sync took 402.
 namespace {
 constexpr int XWT_KS = 2, XWT_SK = XT_TILE, XWT_BUF = XWT_SK + XWT_KS * XT_TILE, XWT_RED = XWT_BUF + 8 * 4096;
