@@ -421,8 +421,9 @@ __device__ __forceinline__ void epilogue_wide(const GemmParams& p, const CUtenso
 // 64.  48000 x 18432 x 768 (1.77 GB of output) takes 815-840 us at 1.4 GHz,
 // 1640 TFLOP/s, and 750 in the first passes from idle: about 4800 clocks a
 // tile of six k-blocks, of which some 1300 are not the main loop's; where they
-// go has not been measured.  6240 x 1280 x 5120 with the residual takes 51 us
-// at 1.97 GHz, three waves of tiles where 2.3 would do.
+// go has not been measured.  6240 x 1280 x 5120 with the residual takes 43 us
+// from L2 and 47-52 with inputs that change, at 1.97 GHz: three waves of tiles
+// where 2.3 would do.
 template <int BN, int EPI, int KIND>
 __global__ void __launch_bounds__(Fp8Shape<BN, epi_wide<EPI>()>::THREADS, 1)
     gemm_fp8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -675,13 +676,13 @@ cudaError_t run_fp8_epi(int epi, bool f16, const CUtensorMap& a, const CUtensorM
 
 cudaError_t launch_linear_fp8(const void* x, const uint8_t* xs, const void* w, const uint8_t* ws, GemmParams p, int epi,
                               bool f16, int num_sms, cudaStream_t st) {
-  // The tile width with the least waves x time of a tile.  A k-block of a
-  // 128 x 32, 128 or 192 tile takes 0.20, 0.25 or 0.29 us alone on its SM
-  // (64 x 1280 x 5120: 10.4, 12.3 and 14.2 us); wider ones move fewer bytes per
-  // product and win once every SM has work (6240 x 1280 x 5120: 128 40.9, 192
-  // 38.0 us; 5 x 768 x 768: 32 4.1, 128 4.5 us; 780 x 1280 x 1280: 128 6.0,
-  // 192 7.1 us).  CTA pairs (256 x 192) were slower throughout: 53.7 us at
-  // 6240 x 1280 x 5120.
+  // The tile width with the least waves x time of a tile, 20 : 25 : 29 a
+  // k-block of a 128 x 32, 128 or 192 tile alone on its SM (64 x 1280 x 5120:
+  // 10.6, 11.3 and 13.1 us); wider ones move fewer bytes per product and win
+  // once every SM has work.  Measured, us, bf16 outputs, inputs that change:
+  // 6240 x 1280 x 5120 114, 42.7, 41.8; 5 x 768 x 768 3.9, 4.3, 4.8; 780 x 1280
+  // x 1280 7.5, 5.8, 6.7.  CTA pairs (256 x 192) were slower throughout: 53.7
+  // at 6240 x 1280 x 5120, where 192 took 38.0 on the same inputs.
   const int mb = (p.M + 127) / 128;
   int bn = 0;
   long long least = 0;
