@@ -144,3 +144,44 @@ def test_threads_at_once_share_a_workspace():
     for a, b in zip(got, ref):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
     assert int(ws.view(torch.int32)[0]) == 0
+
+
+def test_beside_the_encoders_kernels():
+    """Split rows and weights (clusters whose blocks wait for one another), the fp8 product, and the encoder's
+    products and attentions on streams of their own: every result as when run alone."""
+    torch.manual_seed(5)
+    r = lambda *s: torch.randn(*s, device="cuda").bfloat16()  # noqa: E731
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    kw = dict(workspace=ws, check=False)
+    q, k, v = r(100, 768), r(20000, 768), r(20000, 768)
+    cq, ck = _cu(0, 100), _cu(0, 20000)
+    a, w = r(6240, 1280), r(5120, 1280)
+    x, wq = sra.quantize_fp8(r(2000, 1280)), sra.quantize_fp8(r(1280, 1280), 128)
+    qkv, short, long_ = r(3000, 3 * 768), _cu(*range(0, 3001, 100)), _cu(0, 1500, 3000)
+    runs = [lambda: sra.cross_attention(q, k, v, cq, ck, 100, 20000, **kw),
+            lambda: sra.cross_attention(q[:1], k, v, cq[:1].new_tensor([0, 1]), ck, 1, 20000, **kw),
+            lambda: sra.cross_attention_weights(q, k, cq, ck, 100, 20000, **kw),
+            lambda: sra.linear_fp8(*x, *wq, workspace=ws),
+            lambda: sra.linear(a, w),
+            lambda: sra.attention(qkv, short, 12),
+            lambda: sra.attention(qkv, long_, 12)]
+    ref = [f() for f in runs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    got = runs[i]()
+                    if not torch.equal(got, ref[i]):
+                        bad.append(i)
+        except Exception as e:
+            bad.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(runs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+    assert int(ws.view(torch.int32)[0]) == 0
